@@ -1,9 +1,11 @@
-"""Measured cases of two operators of the layer around the attention.
+"""Measured cases of three operators of the layer around the attention.
 
-norm_rope   RMS norm of every query and key head, with the position rotation in the same pass: forward
-            (`sagesla_qk_norm_rope`) and backward (`sagesla_qk_norm_rope_bwd`).
-w8a8_token  linear layer in 8-bit integers, one scale per token of x and per output channel of W
-            (`sagesla_w8a8_token_linear`; the weight is quantised once by `sagesla_w8a8_token_quant`).
+norm_rope     RMS norm of every query and key head, with the position rotation in the same pass: forward
+              (`sagesla_qk_norm_rope`) and backward (`sagesla_qk_norm_rope_bwd`).
+w8a8_token    linear layer in 8-bit integers, one scale per token of x and per output channel of W
+              (`sagesla_w8a8_token_linear`; the weight is quantised once by `sagesla_w8a8_token_quant`).
+linear_decay  causal linear attention with a decay for each head: whole prompts (`sagesla_linear_decay`) and single
+              tokens (`sagesla_linear_decay_step`).
 """
 import torch
 
@@ -24,32 +26,36 @@ def _w8a8(name, dtype, M, N, K, bias):
     return {"name": name, "op": "w8a8_token", "dtype": dtype, "M": M, "N": N, "K": K, "bias": bias}
 
 
+def _decay(name, step, B, N, H, Hk, d, padded, head_major):
+    return {"name": name, "op": "linear_decay_step" if step else "linear_decay", "dtype": "bf16", "B": B, "N": N, "H": H,
+            "Hk": Hk, "d": d, "padded": padded, "head_major": head_major}
+
+
 def listed():
     return [
         # one new token of four sequences, anywhere in a long context, grouped key heads
         _rope("rope_step_b4_h40_8", False, "bf16", 4, 1, 40, 8, 128, 128, False, "tokens", 131072, False),
-        # two padded prompts, a quarter of the channels rotated, fp16
+        # two prompts, one of them padded, a quarter of the channels rotated, fp16
         _rope("rope_prompt_b2_n1000_d64_fp16", False, "fp16", 2, 1000, 16, 4, 64, 16, False, "tokens", 4096, False),
-        # the 1.3B video model at 480p: from the fused projection's rows to the attention's head-major tensors
-        _rope("rope_480p_h12", False, "bf16", 1, 32760, 12, 12, 128, 128, True, "index", 32760, True),
         # the 14B video model at 720p, the token-major form
         _rope("rope_720p_h40", False, "bf16", 1, 75600, 40, 40, 128, 128, True, "index", 75600, False),
-        # training in fp32: odd length, wide heads, grouped key heads, padded rows
-        _rope("rope_bwd_b3_n577_d256_fp32", True, "fp32", 3, 577, 8, 2, 256, 128, False, "tokens", 1024, False),
         # training of the 1.3B video model at 480p
         _rope("rope_bwd_480p_h12", True, "bf16", 1, 32760, 12, 12, 128, 128, True, "index", 32760, True),
         # one token (a timestep's embedding through a projection of the 14B model)
         _w8a8("w8a8_m1_5120", "bf16", 1, 5120, 5120, True),
-        # a few tokens into the feed-forward width of the 14B model
-        _w8a8("w8a8_m24_ffn_fp16", "fp16", 24, 13824, 5120, True),
         # odd sizes: an output width that is no multiple of anything
-        _w8a8("w8a8_m333_n1001_k1280", "fp16", 333, 1001, 1280, True),
+        _w8a8("w8a8_m333_n1001_k1280_fp16", "fp16", 333, 1001, 1280, True),
         # a small clip's tokens through a projection of the 14B model
         _w8a8("w8a8_m1024_5120", "bf16", 1024, 5120, 5120, False),
-        # 480p tokens at the 1.3B model's width
-        _w8a8("w8a8_480p_1536", "bf16", 32760, 1536, 1536, True),
         # 720p tokens at the 14B model's width
         _w8a8("w8a8_720p_5120", "bf16", 75600, 5120, 5120, False),
+        # one new token of one sequence, and of a batch of 64
+        _decay("decay_step_b1_h40", True, 1, 1, 40, 40, 128, False, False),
+        _decay("decay_step_b64_h40", True, 64, 1, 40, 40, 128, False, False),
+        # three prompts of different lengths behind an earlier state, grouped key heads
+        _decay("decay_prompt_b3_n1000_d64", False, 3, 1000, 16, 4, 64, True, False),
+        # a 480p clip's tokens as one causal sequence, the attention's head-major tensors
+        _decay("decay_480p_h12", False, 1, 32760, 12, 12, 128, False, True),
     ]
 
 
@@ -58,7 +64,8 @@ def _log(rng, lo, hi):
 
 
 def draw(rng):
-    if rng.random() < 0.5:
+    op = rng.choice(["norm_rope", "w8a8_token", "linear_decay"])
+    if op == "norm_rope":
         d = rng.choice([32, 64, 80, 128, 128, 256])
         rot = rng.choice([d, d, d // 32 * 16, 16])
         Hk = rng.choice([1, 2, 4, 8, 12])
@@ -70,6 +77,14 @@ def draw(rng):
         T = N if pos == "index" else _log(rng, max(N, 64), 131072)
         return _rope("", rng.random() < 0.5, rng.choice(sorted(DTYPES)), B, N, Hq, Hk, d, rot, rng.random() < 0.5,
                      pos, T, rng.random() < 0.5)
+    if op == "linear_decay":
+        d = rng.choice([64, 128, 128])
+        Hk = rng.choice([1, 2, 4, 8, 12])
+        H = Hk * rng.choice([1, 1, 1, 4])
+        step = rng.random() < 0.4
+        B = _log(rng, 1, 64) if step else rng.randint(1, 4)
+        N = 1 if step else _log(rng, 1, int(32760 * min(1.0, (12 / (B * H)) ** 0.5)))
+        return _decay("", step, B, N, H, Hk, d, not step and rng.random() < 0.5, rng.random() < 0.5)
     N, K = _log(rng, 64, 13824), 16 * _log(rng, 8, 320)
     M = _log(rng, 1, min(32760, 75600 * 5120 * 5120 // (N * K)))
     return _w8a8("", rng.choice(["bf16", "fp16"]), M, N, K, rng.random() < 0.5)
@@ -138,8 +153,31 @@ def _prepare_w8a8(c, seed):
     return {"x": x, "wq": codes.to(torch.int8), "sw": sw, "bias": bias}
 
 
+def _prepare_decay(c, seed):
+    g = _gen(seed)
+    B, N, H, Hk, d = c["B"], c["N"], c["H"], c["Hk"], c["d"]
+
+    def rows(heads):  # normalised rows, as a norm of each head leaves them
+        if c["head_major"]:
+            return torch.randn(B, heads, N, d, device="cuda", generator=g, dtype=torch.bfloat16).transpose(1, 2)
+        return torch.randn(B, N, heads, d, device="cuda", generator=g, dtype=torch.bfloat16)
+    s = {"q": rows(H), "k": rows(Hk), "v": rows(Hk)}
+    # slopes from 2^(-8/H) per token (the last tokens alone) to 2^-8 (hundreds of tokens)
+    s["log_decay"] = -torch.pow(2.0, -8.0 * torch.arange(1, H + 1, device="cuda", dtype=torch.float32) / H)
+    s["scale"] = d ** -0.5
+    s["state"] = 3 * torch.randn(B, H, d, d, device="cuda", generator=g)
+    s["state_out"] = torch.empty_like(s["state"])  # a user keeps two states, or gives the same one twice
+    s["lens"] = None
+    if c["padded"]:
+        s["lens"] = torch.tensor([N] + [max(0, N * 3 // 4 - 100 * i) for i in range(1, B)], device="cuda", dtype=torch.int32)
+    if c["op"] == "linear_decay_step":
+        s.update({n: s[n][:, 0] for n in "qkv"})
+    return s
+
+
 def prepare(case, seed):
-    s = _prepare_w8a8(case, seed) if case["op"] == "w8a8_token" else _prepare_rope(case, seed)
+    make = {"w8a8_token": _prepare_w8a8, "linear_decay": _prepare_decay, "linear_decay_step": _prepare_decay}
+    s = make.get(case["op"], _prepare_rope)(case, seed)
     s["case"] = case
     return s
 
@@ -215,8 +253,66 @@ def _run_w8a8(s):
     return y.to(s["x"].dtype)
 
 
+CHUNK = 128  # tokens that the plain form takes together
+
+
+def _step_plain(c, s):
+    G = c["H"] // c["Hk"]
+    q, k, v = s["q"].float(), s["k"].float().repeat_interleave(G, 1), s["v"].float().repeat_interleave(G, 1)
+    state = s["state"] * torch.exp(s["log_decay"])[:, None, None] + k[..., :, None] * v[..., None, :]
+    out = s["scale"] * (q[..., None, :] @ state)[..., 0, :]
+    return out.to(s["q"].dtype), state
+
+
+def _decay_plain(c, s):
+    """Chunks of 128 tokens: products within a chunk, and the sums of earlier chunks by one product over chunks."""
+    B, N, H, d, G = c["B"], c["N"], c["H"], c["d"], c["H"] // c["Hk"]
+    C, nc = CHUNK, -(-N // CHUNK)
+    lens = s["lens"].long() if s["lens"] is not None else torch.full((B,), N, device="cuda")
+    real = (torch.arange(nc * C, device="cuda") < lens[:, None])[:, None, :, None]
+
+    def chunks(x, heads):  # [B, H, nc, C, d] in 32 bits, rows past a sequence's end 0
+        x = x.float().transpose(1, 2).repeat_interleave(heads, 1)
+        return torch.where(real, torch.nn.functional.pad(x, (0, 0, 0, nc * C - N)), 0.0).unflatten(2, (nc, C))
+    q, k, v = chunks(s["q"], 1), chunks(s["k"], G), chunks(s["v"], G)
+    g = s["log_decay"].double()[:, None, None]
+    i = torch.arange(C, device="cuda", dtype=torch.float64)
+    j = torch.arange(nc, device="cuda", dtype=torch.float64)
+    diff = i[:, None] - i[None]
+    within = torch.where(diff >= 0, torch.exp(g * diff.clamp(min=0)), 0.0).float()[:, None]  # [H, 1, C, C]
+    out = ((q @ k.transpose(-1, -2)) * within) @ v
+    to_end = torch.exp(g[..., 0] * (C - 1 - i)).float()[:, None, :, None]
+    sums = ((k * to_end).transpose(-1, -2) @ v).flatten(3)  # what each chunk adds to the state, [B, H, nc, d*d]
+    gap = j[:, None] - j[None] - 1
+    across = torch.where(gap >= 0, torch.exp(g * C * gap.clamp(min=0)), 0.0).float()  # [H, nc, nc]
+    state = across @ sums + torch.exp(g[..., 0] * C * j).float()[..., None] * s["state"].flatten(2)[:, :, None]
+    out += (q * torch.exp(g[..., 0] * (i + 1)).float()[:, None, :, None]) @ state.unflatten(3, (d, d))
+    out = (s["scale"] * out).flatten(2, 3)[:, :, :N].to(s["q"].dtype)
+    # the state behind a sequence's last token: its chunk's start, and the chunk's own tokens decayed to that token
+    last = torch.div(lens.clamp(min=1) - 1, C, rounding_mode="floor")
+    n = (lens - last * C).double()[:, None, None]  # tokens of the last chunk
+    b = torch.arange(B, device="cuda")
+    weight = torch.where(i < n, torch.exp(g[..., 0] * (n - 1 - i).clamp(min=0)), 0.0).float()  # [B, H, C]
+    end = torch.exp(g[..., 0] * n).float()[..., None] * state.unflatten(3, (d, d))[b, :, last]
+    end = end + (k[b, :, last] * weight[..., None]).transpose(-1, -2) @ v[b, :, last]
+    return (out if c["head_major"] else out.transpose(1, 2)), end
+
+
+def _run_decay(s):
+    c = s["case"]
+    if own:
+        import sparse_bit_attention_smoothing_b200 as sg
+        if c["op"] == "linear_decay_step":
+            return sg.sagesla_linear_decay_step(s["q"], s["k"], s["v"], s["log_decay"], s["state"], scale=s["scale"],
+                                                state_out=s["state_out"])
+        return sg.sagesla_linear_decay(s["q"], s["k"], s["v"], s["log_decay"], s["state"], lens=s["lens"],
+                                       scale=s["scale"], state_out=s["state_out"], head_major=c["head_major"])
+    return _step_plain(c, s) if c["op"] == "linear_decay_step" else _decay_plain(c, s)
+
+
 def run(state):
-    return _run_w8a8(state) if state["case"]["op"] == "w8a8_token" else _run_rope(state)
+    op = state["case"]["op"]
+    return _run_w8a8(state) if op == "w8a8_token" else _run_decay(state) if op.startswith("linear") else _run_rope(state)
 
 
 def work(case):
@@ -225,6 +321,11 @@ def work(case):
         M, N, K = c["M"], c["N"], c["K"]
         return {"bytes": M * K * e + N * K + 4 * N + (e * N if c["bias"] else 0) + M * N * e, "flops": 2 * M * N * K}
     tokens = c["B"] * c["N"]
+    if c["op"].startswith("linear"):
+        d, H = c["d"], c["H"]
+        moved = tokens * (2 * H + 2 * c["Hk"]) * d * e + 2 * c["B"] * H * d * d * 4 + 4 * H
+        # a token: its product with the state and its outer product, 2 d^2 each
+        return {"bytes": moved, "flops": 4 * tokens * H * d * d}
     rows = tokens * (c["Hq"] + c["Hk"])
     back = c["op"] == "norm_rope_bwd"
     table = min(c["T"], tokens) * c["rot"] * 4
@@ -278,6 +379,33 @@ def _exact_w8a8(s):
     return y if s["bias"] is None else y + s["bias"].double()
 
 
+def _exact_decay(c, s):
+    """The sum over all earlier tokens, a block of queries at a time (quadratic in the length)."""
+    step = c["op"] == "linear_decay_step"
+    q, k, v = (s[n].double() if step else s[n].double().transpose(1, 2) for n in "qkv")
+    if step:
+        q, k, v = q[:, :, None], k[:, :, None], v[:, :, None]
+    B, N, H, G = c["B"], c["N"], c["H"], c["H"] // c["Hk"]
+    k, v = k.repeat_interleave(G, 1), v.repeat_interleave(G, 1)
+    g, S0 = s["log_decay"].double(), s["state"].double()
+    out, end = torch.zeros_like(q), torch.empty_like(S0)
+    for b in range(B):
+        n = N if s["lens"] is None else int(s["lens"][b])
+        t = torch.arange(n, device="cuda", dtype=torch.float64)
+        for i in range(0, n, 512):
+            e = min(n, i + 512)
+            age = t[i:e, None] - t[None, :e]
+            w = q[b, :, i:e] @ k[b, :, :e].transpose(-1, -2)
+            w *= torch.exp(g[:, None, None] * age.clamp(min=0)).masked_fill_(age < 0, 0)
+            old = torch.exp(g[:, None] * (t[i:e] + 1))[..., None] * (q[b, :, i:e] @ S0[b])
+            out[b, :, i:e] = s["scale"] * (w @ v[b, :, :e] + old)
+        left = torch.exp(g[:, None] * (n - 1 - t))[..., None] * k[b, :, :n]
+        end[b] = left.transpose(-1, -2) @ v[b, :, :n] + torch.exp(g * n)[:, None, None] * S0[b]
+    return (out[:, :, 0] if step else out if c["head_major"] else out.transpose(1, 2)), end
+
+
 def exact(case, seed):
     s = prepare(case, seed)
+    if case["op"].startswith("linear"):
+        return _exact_decay(case, s)
     return _exact_w8a8(s) if case["op"] == "w8a8_token" else _exact_rope(case, s)

@@ -288,6 +288,124 @@ int sagesla_w8a8_gemm(const void* xq, const float* sx, const void* wq, const flo
 int sagesla_w8a8_linear(const void* x, const void* wq, const float* sw, void* y, int M, int N, int K,
                         sagesla_stream_t stream);
 
+/* Element types of the entry points below. */
+enum { SAGESLA_BF16 = 0, SAGESLA_FP16 = 1, SAGESLA_FP32 = 2 };
+
+/*
+ * W8A8 linear layer with one scale per token and per output channel:
+ * y = x W^T + bias, x [M][K] and W [N][K] INT8.  Beside the 128 x 128 form
+ * above it keeps a scale for every row of x and of W (finer along M and N,
+ * coarser along K), takes codes in plain row-major order (as other programs
+ * store them), any M and N, and runs the whole of K in integers:
+ *   per row: amax = largest magnitude, s = fl32(amax/127),
+ *   code = RNE(fl32(v * fl32(127/amax))) clamped to +-127; a row with
+ *   amax < 2^-100 has s = 1 and codes 0; a row with NaN or an infinity has
+ *   s = NaN and codes 0 (its outputs are NaN);
+ *   y[m][n] = fl32(dot) * s_x[m] * s_w[n] + bias[n] in fp32, the dot an exact
+ *   INT32 sum, rounded once to y's type.
+ * sagesla_w8a8_token_quant: codes int8 [rows][cols] and scales fp32 [rows] of
+ *   a bf16 or fp16 (dtype) device matrix whose rows start `lda` elements
+ *   apart (lda >= cols, a multiple of 8).  cols a multiple of 16, at most
+ *   131056.  For W once, and for x.
+ * sagesla_w8a8_token_gemm: y ([M][N], dtype) from codes and scales; codes may
+ *   use the whole of int8.  bias [N] of y's type or NULL.
+ * sagesla_w8a8_token_linear: quantises x (dtype, rows ldx elements apart)
+ *   into the caller's workspace, then the product into y of x's type.  The
+ *   workspace (sagesla_w8a8_token_workspace tells its bytes; 16-byte aligned)
+ *   belongs to the call until it has run: calls on other streams, and graphs that may run
+ *   at the same time, need their own.  Nothing else is allocated, so the call
+ *   can be captured.
+ * K a multiple of 16 (16 .. 131056); M, N from 1 to 8388480.  a, x, codes, y
+ * 16-byte aligned, scales 4-byte, bias 2-byte.  Codes of sagesla_attn.
+ */
+int sagesla_w8a8_token_quant(const void* a, int dtype, int rows, int cols, long long lda, int8_t* codes, float* scales,
+                             sagesla_stream_t stream);
+int sagesla_w8a8_token_gemm(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, const void* bias,
+                            void* y, int dtype, int M, int N, int K, sagesla_stream_t stream);
+int sagesla_w8a8_token_workspace(int M, int K, long long* bytes);
+int sagesla_w8a8_token_linear(const void* x, long long ldx, const int8_t* wq, const float* sw, const void* bias,
+                              void* y, int dtype, int M, int N, int K, void* workspace, long long workspace_bytes,
+                              sagesla_stream_t stream);
+
+/*
+ * sagesla_qk_norm_rope: RMS norm of every query and key head and the position
+ * rotation, in one pass over q and k (what stands between a DiT's projections
+ * and sagesla_attn where the norm is taken per head; sagesla_attn_qknorm is
+ * the norm over all heads).  Per row of d channels, in fp32:
+ *   n = x / sqrt(mean(x^2) + eps) * gamma   (gamma_q / gamma_k: [d] of the
+ *       tensors' type, shared by the heads),
+ *   the first `rot` channels turned in pairs by the token's position p,
+ *   (a, b) -> (a cos - b sin, a sin + b cos) with pair c = channels
+ *   (2c, 2c+1) (interleaved = 1) or (c, c + rot/2) (interleaved = 0) and
+ *   cos[p][c], sin[p][c]; the other channels pass; rounded once.
+ *   q, k, q_out, k_out   dtype (bf16, fp16, fp32), rows [b][n][h] of d
+ *            channels at strides[] elements: strides is a host array of 12,
+ *            (batch, token, head) of q, k, q_out, k_out.  So q and k may be
+ *            views of a fused projection, and the outputs token-major or
+ *            head-major.  An output is exactly its input (same pointer and
+ *            strides) or overlaps no input.
+ *   Hq, Hk   heads of q and k; Hk = 0: no k (k, gamma_k, k_out ignored).
+ *   cos, sin fp32 [T][rot/2] device; unused for rot = 0.
+ *   pos      int32 [B][N] device: a position of each token, or NULL: the
+ *            token's index n (then N <= T).  A token with pos < 0 is padding:
+ *            it is not read and its outputs are 0.  pos >= T: its outputs are
+ *            NaN (the tables are not read out of range).
+ * d a multiple of 16 from 16 to 256, rot a multiple of 16 from 0 to d; eps in
+ * [0, 1]; B*N < 2^31, Hq, Hk <= 65535, B*N*(Hq+Hk) < 2^33.  Pointers 16-byte
+ * aligned, strides multiples of 16 bytes and not negative; the rows of an
+ * output must not overlap.  |x| below 2^60 (squares are summed in fp32).
+ * Nothing is allocated: the call can be captured.  Codes as sagesla_attn.
+ *
+ * sagesla_qk_norm_rope_bwd: its backward pass.  dq_out, dk_out: gradients of
+ * q_out, k_out; dq, dk: gradients of q, k (rows at strides[12..17]; the array
+ * has 18: dq_out, dk_out, q, k, dq, dk); dgamma_q, dgamma_k: fp32 [d], summed
+ * over every row in a fixed order (the same bits every time).  Padding tokens
+ * get gradient 0 and add nothing; pos >= T gives NaN.  dq may be exactly
+ * dq_out or q.  workspace: the bytes that
+ * sagesla_qk_norm_rope_bwd_workspace tells for the current device, 16-byte
+ * aligned, the call's own until it has run.
+ */
+int sagesla_qk_norm_rope(const void* q, const void* k, const void* gamma_q, const void* gamma_k, float eps,
+                         const float* cos, const float* sin, const int32_t* pos, void* q_out, void* k_out, int dtype,
+                         int B, int N, int Hq, int Hk, int d, int rot, int T, int interleaved,
+                         const int64_t* strides, sagesla_stream_t stream);
+int sagesla_qk_norm_rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, long long* bytes);
+int sagesla_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                             const void* gamma_q, const void* gamma_k, float eps, const float* cos, const float* sin,
+                             const int32_t* pos, void* dq, void* dk, float* dgamma_q, float* dgamma_k, int dtype,
+                             int B, int N, int Hq, int Hk, int d, int rot, int T, int interleaved,
+                             const int64_t* strides, void* workspace, long long workspace_bytes,
+                             sagesla_stream_t stream);
+
+/*
+ * Causal linear attention with a decay for each head: the streaming form of
+ * the linear branch, whose sums over tokens become a state that a clip's next
+ * tokens continue.  Per sequence b and head h, with key head h / (H/Hk):
+ *   S_t = e^{log_decay[h]} S_{t-1} + k_t v_t^T,   out_t = scale * q_t^T S_t,
+ * S [d channels of k][d of v] in fp32; out rounded once to bf16.
+ * sagesla_linear_decay: whole prompts.
+ *   q, k, v, out  bf16, rows [b][n][h] of d channels at strides[] elements (a
+ *            host array of 12: batch, token, head of q, k, v, out).
+ *   log_decay fp32 [H] device, <= 0 (-infinity: only the token itself).
+ *   state_in fp32 [B][H][d][d] device: S before the first token; NULL: 0.
+ *   state_out the same shape: S behind each sequence's last token (may be
+ *            state_in); NULL: not kept.
+ *   lens     int32 [B] device: tokens of each sequence (taken into [0, N]);
+ *            NULL: N.  Rows at and past the length are not read and their
+ *            out is 0; a length of 0 leaves the state as it was.
+ * sagesla_linear_decay_step: one token of each sequence (N = 1); strides is a
+ *   host array of 8: batch, head of q, k, v, out.
+ * d 64 or 128; Hk divides H; B*H <= 65535.  Pointers 16-byte aligned, strides
+ * multiples of 8 elements and not negative, the rows of out apart; out
+ * overlaps no input.  Codes as sagesla_attn.
+ */
+int sagesla_linear_decay(const void* q, const void* k, const void* v, const float* log_decay, const float* state_in,
+                         const int32_t* lens, float scale, void* out, float* state_out, int B, int N, int H, int Hk,
+                         int d, const int64_t* strides, sagesla_stream_t stream);
+int sagesla_linear_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
+                              const float* state_in, float scale, void* out, float* state_out, int B, int H, int Hk,
+                              int d, const int64_t* strides, sagesla_stream_t stream);
+
 /* Human-readable text for a return code (static storage). */
 const char* sagesla_strerror(int code);
 
@@ -300,11 +418,13 @@ const char* sagesla_strerror(int code);
  * 3 pooled top-k, 4 linear per-block phi(K)^T V, 5 linear complement sum,
  * 6 sparse flash, 7 projection-weight tiling, 8 linear output (phi(Q) H,
  * normalisation, projection), 9 W8A8 block quantiser, 10 W8A8 GEMM,
- * 11 QK RMSNorm per-token sums.
+ * 11 QK RMSNorm per-token sums, 12 row quantiser, 13 per-token/channel W8A8
+ * product, 14 QK norm and rotation, 15 its backward pass, 16 linear attention
+ * with a decay (prompts), 17 the same (single tokens).
  * ms / launches are arrays of nkernels entries (either may be NULL).
  * Profiling is off by default.
  */
-#define SAGESLA_NUM_KERNELS 12
+#define SAGESLA_NUM_KERNELS 18
 void sagesla_profile(int enable);
 int sagesla_profile_read(double* ms, int* launches, int nkernels);
 

@@ -30,9 +30,13 @@ class SageSLAError(RuntimeError):
 EXPORTS = ["sagesla_attn", "sagesla_attn_opts", "sagesla_attn_qknorm", "sagesla_attn_bnhd", "dense_int8_attn", "sagesla_attn_host", "sagesla_get_quant", "sagesla_get_mask",
            "sagesla_smooth_stats_noalloc", "sagesla_topk_count", "sagesla_sync_status", "sagesla_strerror",
            "sagesla_release", "sagesla_profile", "sagesla_profile_read", "sagesla_watchdog_selftest",
-           "sagesla_debug_flash_stall", "sagesla_w8a8_quant", "sagesla_w8a8_gemm", "sagesla_w8a8_linear"]
+           "sagesla_debug_flash_stall", "sagesla_w8a8_quant", "sagesla_w8a8_gemm", "sagesla_w8a8_linear",
+           "sagesla_w8a8_token_quant", "sagesla_w8a8_token_gemm", "sagesla_w8a8_token_workspace",
+           "sagesla_w8a8_token_linear", "sagesla_qk_norm_rope", "sagesla_qk_norm_rope_bwd",
+           "sagesla_qk_norm_rope_bwd_workspace", "sagesla_linear_decay", "sagesla_linear_decay_step"]
 KERNELS = ["stats", "stats_final", "quant", "pool_topk", "linear_kv", "linear_sum", "flash", "w_tile",
-           "linear_apply", "w8a8_quant", "w8a8_gemm", "rms_inv"]
+           "linear_apply", "w8a8_quant", "w8a8_gemm", "rms_inv", "w8a8_token_quant", "w8a8_token_gemm",
+           "qk_norm_rope", "qk_norm_rope_bwd", "linear_decay", "linear_decay_step"]
 
 
 def lib():
@@ -59,6 +63,16 @@ def lib():
         L.sagesla_w8a8_quant.argtypes = [P, i, i, P, P, P]
         L.sagesla_w8a8_gemm.argtypes = [P, P, P, P, P, i, i, i, P]
         L.sagesla_w8a8_linear.argtypes = [P, P, P, P, i, i, i, P]
+        ll = ctypes.c_longlong
+        L.sagesla_w8a8_token_quant.argtypes = [P, i, i, i, ll, P, P, P]
+        L.sagesla_w8a8_token_gemm.argtypes = [P, P, P, P, P, P, i, i, i, i, P]
+        L.sagesla_w8a8_token_workspace.argtypes = [i, i, P]
+        L.sagesla_w8a8_token_linear.argtypes = [P, ll, P, P, P, P, i, i, i, i, P, ll, P]
+        L.sagesla_qk_norm_rope.argtypes = [P, P, P, P, f, P, P, P, P, P, i, i, i, i, i, i, i, i, i, P, P]
+        L.sagesla_qk_norm_rope_bwd_workspace.argtypes = [i, i, i, i, i, P]
+        L.sagesla_qk_norm_rope_bwd.argtypes = [P, P, P, P, P, P, f, P, P, P, P, P, P, P, i, i, i, i, i, i, i, i, i, P, P, ll, P]
+        L.sagesla_linear_decay.argtypes = [P, P, P, P, P, P, f, P, P, i, i, i, i, i, P, P]
+        L.sagesla_linear_decay_step.argtypes = [P, P, P, P, P, f, P, P, i, i, i, i, P, P]
         L.sagesla_strerror.restype = ctypes.c_char_p
         L.sagesla_strerror.argtypes = [i]
         L.sagesla_release.restype = None
@@ -277,6 +291,284 @@ def sagesla_w8a8_linear(x, wq, sw, N: int, y=None, stream=None):
     _check(lib().sagesla_w8a8_linear(_ptr(x), _ptr(wq), _ptr(sw), _ptr(y), M, N, K, _stream(stream)),
            "sagesla_w8a8_linear")
     return y
+
+
+# ---- operators of the layer around the attention --------------------------
+# Tensors are checked here (types, shapes, one device), the rest by the
+# library.  Work runs on `stream` (default: the tensors' device's current
+# stream), with that device current for the call; what a call allocates (its
+# outputs and workspace) is allocated on that stream.
+
+def _dtype(t, fp32=False):
+    import torch
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2 if fp32 else None}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{t.dtype} is not supported (bfloat16, float16{', float32' if fp32 else ''})")
+    return code
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+class _On:
+    """The device and stream of a call: `.s` is the stream's handle."""
+
+    def __init__(self, t, stream, *others):
+        import torch
+        _need(t.is_cuda, "CUDA tensors are needed")
+        for o in others:
+            _need(o is None or o.device == t.device, "the tensors are on different devices")
+        self.ctx = None
+        if stream is not None:
+            _need(stream.device == t.device, "the stream is on another device than the tensors")
+            self.ctx = torch.cuda.stream(stream)  # makes its device current too
+        elif torch.cuda.current_device() != t.device.index:
+            self.ctx = torch.cuda.device(t.device)
+        self.s = (stream if stream is not None else torch.cuda.current_stream(t.device)).cuda_stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self
+
+    def __exit__(self, *e):
+        if self.ctx is not None:
+            self.ctx.__exit__(*e)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _vector(t, n, dtype, what):
+    _need(t.dtype == dtype and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
+          f"{what} must be a contiguous {dtype} vector of {n}")
+
+
+def sagesla_w8a8_token_quant(a, stream=None):
+    """INT8 codes [rows, cols] (row-major) and fp32 scales [rows] of a bf16 or fp16 CUDA matrix, one scale a row."""
+    import torch
+    _need(a.dim() == 2 and a.stride(1) == 1, "a must be a matrix with contiguous rows")
+    dt = _dtype(a)
+    rows, cols = a.shape
+    with _On(a, stream) as on:
+        codes = torch.empty(rows, cols, dtype=torch.int8, device=a.device)
+        scales = torch.empty(rows, dtype=torch.float32, device=a.device)
+        _check(lib().sagesla_w8a8_token_quant(_p(a), dt, rows, cols, a.stride(0), _p(codes), _p(scales), on.s),
+               "sagesla_w8a8_token_quant")
+    return codes, scales
+
+
+def _token_weight(wq, sw, bias, K, dtype):
+    import torch
+    _need(wq.dim() == 2 and wq.dtype == torch.int8 and wq.is_contiguous() and wq.shape[1] == K,
+          f"wq must be a contiguous int8 [N, {K}] matrix")
+    N = wq.shape[0]
+    _vector(sw, N, torch.float32, "sw")
+    if bias is not None:
+        _vector(bias, N, dtype, "bias")
+    return N
+
+
+def _token_out(y, M, N, dtype, device):
+    import torch
+    if y is None:
+        return torch.empty(M, N, dtype=dtype, device=device)
+    _need(y.shape == (M, N) and y.dtype == dtype and y.is_contiguous(), f"y must be a contiguous {dtype} [{M}, {N}]")
+    return y
+
+
+def sagesla_w8a8_token_gemm(xq, sx, wq, sw, bias=None, dtype=None, y=None, stream=None):
+    """y = (xq . wq^T) sx sw + bias, [M, N] of `dtype` (y's, or bf16): codes int8 [M, K] and [N, K], scales fp32
+    [M] and [N]."""
+    import torch
+    dtype = dtype or (y.dtype if y is not None else torch.bfloat16)
+    _need(xq.dim() == 2 and xq.dtype == torch.int8 and xq.is_contiguous(), "xq must be a contiguous int8 [M, K] matrix")
+    M, K = xq.shape
+    _vector(sx, M, torch.float32, "sx")
+    N = _token_weight(wq, sw, bias, K, dtype)
+    with _On(xq, stream, sx, wq, sw, bias, y) as on:
+        y = _token_out(y, M, N, dtype, xq.device)
+        _check(lib().sagesla_w8a8_token_gemm(_p(xq), _p(sx), _p(wq), _p(sw), _p(bias), _p(y), _dtype(y), M, N, K, on.s),
+               "sagesla_w8a8_token_gemm")
+    return y
+
+
+def sagesla_w8a8_token_workspace(M: int, K: int) -> int:
+    """Bytes of workspace that one sagesla_w8a8_token_linear call uses."""
+    n = ctypes.c_longlong(0)
+    _check(lib().sagesla_w8a8_token_workspace(M, K, ctypes.byref(n)), "sagesla_w8a8_token_workspace")
+    return n.value
+
+
+def sagesla_w8a8_token_linear(x, wq, sw, bias=None, y=None, stream=None):
+    """The linear layer in 8-bit integers, a scale per token of x (bf16 or fp16 [M, K]) and per output channel of the
+    weight (codes and scales of sagesla_w8a8_token_quant): y [M, N] of x's type."""
+    import torch
+    _need(x.dim() == 2 and x.stride(1) == 1, "x must be a matrix with contiguous rows")
+    dt = _dtype(x)
+    M, K = x.shape
+    N = _token_weight(wq, sw, bias, K, x.dtype)
+    with _On(x, stream, wq, sw, bias, y) as on:
+        y = _token_out(y, M, N, x.dtype, x.device)
+        nb = sagesla_w8a8_token_workspace(M, K)
+        ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+        _check(lib().sagesla_w8a8_token_linear(_p(x), x.stride(0), _p(wq), _p(sw), _p(bias), _p(y), dt, M, N, K,
+                                               _p(ws), nb, on.s), "sagesla_w8a8_token_linear")
+    return y
+
+
+def _rows4(t, B, N, d, dtype, what):
+    _need(t.dim() == 4 and t.shape[0] == B and t.shape[1] == N and t.shape[3] == d and t.dtype == dtype
+          and t.stride(3) == 1, f"{what} must be a {dtype} [{B}, {N}, heads, {d}] tensor with contiguous channels")
+    return t.shape[2]
+
+
+def _strides(*ts):
+    s = [v for t in ts for v in (t.stride()[:3] if t is not None else (0, 0, 0))]
+    return (ctypes.c_int64 * len(s))(*s)
+
+
+def _rope_args(q, k, gamma_q, gamma_k, cos, sin, pos):
+    """(B, N, Hq, Hk, d, rot, T) of the checked tensors of a norm-and-rotation call."""
+    import torch
+    _need(q.dim() == 4, "q must be [B, N, H, d]")
+    B, N, Hq, d = q.shape
+    _rows4(q, B, N, d, q.dtype, "q")
+    Hk = 0 if k is None else _rows4(k, B, N, d, q.dtype, "k")
+    _vector(gamma_q, d, q.dtype, "gamma_q")
+    if k is not None:
+        _need(gamma_k is not None, "k needs gamma_k")
+        _vector(gamma_k, d, q.dtype, "gamma_k")
+    _need(cos.dim() == 2 and cos.shape == sin.shape and cos.dtype == sin.dtype == torch.float32
+          and cos.is_contiguous() and sin.is_contiguous(), "cos and sin must be contiguous fp32 [T, rot/2] tables")
+    if pos is not None:
+        _need(pos.dtype == torch.int32 and pos.shape == (B, N) and pos.is_contiguous(),
+              f"pos must be a contiguous int32 [{B}, {N}] tensor")
+    return B, N, Hq, Hk, d, 2 * cos.shape[1], cos.shape[0]
+
+
+def _rows_out(t, B, N, H, d, like, head_major, what):
+    import torch
+    if t is not None:
+        _need(_rows4(t, B, N, d, like.dtype, what) == H, f"{what} must have {H} heads")
+        return t
+    shape = (B, H, N, d) if head_major else (B, N, H, d)
+    t = torch.empty(shape, dtype=like.dtype, device=like.device)
+    return t.transpose(1, 2) if head_major else t
+
+
+def sagesla_qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, pos=None, eps: float = 1e-6, interleaved: bool = True,
+                         q_out=None, k_out=None, head_major: bool = False, stream=None):
+    """RMS norm of every query and key head and the position rotation, in one pass.  q [B, N, Hq, d] and k
+    [B, N, Hk, d] (k None: q alone) bf16, fp16 or fp32 with any strides (views of a fused projection); gamma_* [d];
+    cos, sin fp32 [T, rot/2], the first rot channels turned in pairs (2c, 2c+1) (interleaved) or (c, c + rot/2); pos
+    int32 [B, N] (None: the token index; negative: padding, outputs 0).  Returns (q_out, k_out), [B, N, H, d], or
+    [B, H, N, d] as sagesla_attn takes it with head_major; q_out, k_out: [B, N, H, d] views to write to."""
+    B, N, Hq, Hk, d, rot, T = _rope_args(q, k, gamma_q, gamma_k, cos, sin, pos)
+    with _On(q, stream, k, gamma_q, gamma_k, cos, sin, pos, q_out, k_out) as on:
+        qo = _rows_out(q_out, B, N, Hq, d, q, head_major, "q_out")
+        ko = None if k is None else _rows_out(k_out, B, N, Hk, d, q, head_major, "k_out")
+        _check(lib().sagesla_qk_norm_rope(_p(q), _p(k), _p(gamma_q), _p(gamma_k), eps, _p(cos), _p(sin), _p(pos), _p(qo),
+                                          _p(ko), _dtype(q, True), B, N, Hq, Hk, d, rot, T, 1 if interleaved else 0,
+                                          _strides(q, k, qo, ko), on.s), "sagesla_qk_norm_rope")
+    if head_major:
+        return qo.transpose(1, 2), None if ko is None else ko.transpose(1, 2)
+    return qo, ko
+
+
+def sagesla_qk_norm_rope_bwd_workspace(B: int, N: int, Hq: int, Hk: int, d: int) -> int:
+    """Bytes of workspace that one sagesla_qk_norm_rope_bwd call uses on the current device."""
+    n = ctypes.c_longlong(0)
+    _check(lib().sagesla_qk_norm_rope_bwd_workspace(B, N, Hq, Hk, d, ctypes.byref(n)),
+           "sagesla_qk_norm_rope_bwd_workspace")
+    return n.value
+
+
+def sagesla_qk_norm_rope_bwd(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, pos=None, eps: float = 1e-6,
+                             interleaved: bool = True, dq=None, dk=None, stream=None):
+    """Backward pass of sagesla_qk_norm_rope: dq_out, dk_out [B, N, H, d] (any strides) are the gradients of its
+    outputs.  Returns (dq, dk, dgamma_q, dgamma_k), dq and dk [B, N, H, d] of q's type, dgamma_* fp32 [d]."""
+    import torch
+    B, N, Hq, Hk, d, rot, T = _rope_args(q, k, gamma_q, gamma_k, cos, sin, pos)
+    _need(_rows4(dq_out, B, N, d, q.dtype, "dq_out") == Hq, f"dq_out must have {Hq} heads")
+    if k is None:
+        dk_out = dk = None
+    else:
+        _need(dk_out is not None and _rows4(dk_out, B, N, d, q.dtype, "dk_out") == Hk, f"dk_out must have {Hk} heads")
+    with _On(q, stream, dq_out, dk_out, k, gamma_q, gamma_k, cos, sin, pos, dq, dk) as on:
+        dq = _rows_out(dq, B, N, Hq, d, q, False, "dq")
+        dk = None if k is None else _rows_out(dk, B, N, Hk, d, q, False, "dk")
+        dg = torch.empty(2, d, dtype=torch.float32, device=q.device)
+        nb = sagesla_qk_norm_rope_bwd_workspace(B, N, Hq, Hk, d)
+        ws = torch.empty(nb, dtype=torch.uint8, device=q.device)
+        _check(lib().sagesla_qk_norm_rope_bwd(_p(dq_out), _p(dk_out), _p(q), _p(k), _p(gamma_q), _p(gamma_k), eps,
+                                              _p(cos), _p(sin), _p(pos), _p(dq), _p(dk), _p(dg[0]), _p(dg[1]),
+                                              _dtype(q, True), B, N, Hq, Hk, d, rot, T, 1 if interleaved else 0,
+                                              _strides(dq_out, dk_out, q, k, dq, dk), _p(ws), nb, on.s),
+               "sagesla_qk_norm_rope_bwd")
+    return dq, dk, dg[0], None if k is None else dg[1]
+
+
+def _decay_state(t, B, H, d, what):
+    import torch
+    _need(t.dtype == torch.float32 and t.shape == (B, H, d, d) and t.is_contiguous(),
+          f"{what} must be a contiguous fp32 [{B}, {H}, {d}, {d}] tensor")
+
+
+def sagesla_linear_decay(q, k, v, log_decay, state=None, lens=None, scale: float = 1.0, out=None, state_out=None,
+                         head_major: bool = False, stream=None):
+    """Causal linear attention with a decay for each head over whole prompts: S = e^log_decay S + k v^T, out =
+    scale q S.  q [B, N, H, d], k, v [B, N, Hk, d] bf16 with any strides; log_decay fp32 [H]; state fp32
+    [B, H, d, d] before the first token (None: zeros); lens int32 [B] (None: N; out of later rows is 0).  Returns (out,
+    state_out): out [B, N, H, d] ([B, H, N, d] with head_major), the state behind the last tokens."""
+    import torch
+    _need(q.dim() == 4 and q.dtype == torch.bfloat16, "q must be a bf16 [B, N, H, d] tensor")
+    B, N, H, d = q.shape
+    _rows4(q, B, N, d, q.dtype, "q")
+    Hk = _rows4(k, B, N, d, q.dtype, "k")
+    _need(_rows4(v, B, N, d, q.dtype, "v") == Hk, "k and v must have the same heads")
+    _vector(log_decay, H, torch.float32, "log_decay")
+    if state is not None:
+        _decay_state(state, B, H, d, "state")
+    if lens is not None:
+        _vector(lens, B, torch.int32, "lens")
+    with _On(q, stream, k, v, log_decay, state, lens, out, state_out) as on:
+        o = _rows_out(out, B, N, H, d, q, head_major, "out")
+        if state_out is None:
+            state_out = torch.empty(B, H, d, d, dtype=torch.float32, device=q.device)
+        _decay_state(state_out, B, H, d, "state_out")
+        _check(lib().sagesla_linear_decay(_p(q), _p(k), _p(v), _p(log_decay), _p(state), _p(lens), scale, _p(o),
+                                          _p(state_out), B, N, H, Hk, d, _strides(q, k, v, o), on.s),
+               "sagesla_linear_decay")
+    return (o.transpose(1, 2) if head_major else o), state_out
+
+
+def sagesla_linear_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, state_out=None, stream=None):
+    """One token of sagesla_linear_decay: q [B, H, d], k, v [B, Hk, d] bf16; state fp32 [B, H, d, d] is updated in
+    place unless state_out is given.  Returns (out [B, H, d], the new state)."""
+    import torch
+    _need(q.dim() == 3 and q.dtype == torch.bfloat16 and q.stride(2) == 1, "q must be a bf16 [B, H, d] tensor")
+    B, H, d = q.shape
+    for t, what in ((k, "k"), (v, "v")):
+        _need(t.dim() == 3 and t.dtype == torch.bfloat16 and t.shape[0] == B and t.shape[2] == d and t.stride(2) == 1
+              and t.shape[1] == k.shape[1], f"{what} must be a bf16 [{B}, Hk, {d}] tensor")
+    _vector(log_decay, H, torch.float32, "log_decay")
+    _decay_state(state, B, H, d, "state")
+    with _On(q, stream, k, v, log_decay, state, out, state_out) as on:
+        if out is None:
+            out = torch.empty(B, H, d, dtype=torch.bfloat16, device=q.device)
+        _need(out.shape == q.shape and out.dtype == torch.bfloat16 and out.stride(2) == 1, "out must be like q")
+        if state_out is None:
+            state_out = state
+        _decay_state(state_out, B, H, d, "state_out")
+        s = [x for t in (q, k, v, out) for x in t.stride()[:2]]
+        _check(lib().sagesla_linear_decay_step(_p(q), _p(k), _p(v), _p(log_decay), _p(state), scale, _p(out),
+                                               _p(state_out), B, H, k.shape[1], d, (ctypes.c_int64 * 8)(*s), on.s),
+               "sagesla_linear_decay_step")
+    return out, state_out
 
 
 def sync_status(stream=None) -> int:

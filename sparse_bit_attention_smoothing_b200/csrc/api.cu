@@ -33,6 +33,11 @@ std::map<std::pair<int, cudaStream_t>, Workspace> g_stage;  // host entry point'
 std::map<int, int*> g_wd;        // per-device watchdog word
 std::map<int, int> g_dev_ok;     // per-device: 1 = sm_100, 0 = not
 
+// The watchdog word is static device storage (zero when the library is
+// loaded), so that finding it allocates nothing and is allowed while a stream
+// of this thread is being captured.
+__device__ int g_wd_word;
+
 int check_device(int* dev_out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SAGESLA_ERR_NO_DEVICE;
@@ -48,10 +53,16 @@ int check_device(int* dev_out) {
   }
   if (!it->second) return SAGESLA_ERR_NO_DEVICE;
   if (!g_wd.count(dev)) {
-    int* wd = nullptr;
-    if (cudaMalloc(&wd, sizeof(int)) != cudaSuccess) return SAGESLA_ERR_OOM;
-    if (cudaMemset(wd, 0, sizeof(int)) != cudaSuccess) return SAGESLA_ERR_LAUNCH;
-    g_wd[dev] = wd;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    void* wd = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&wd, g_wd_word);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return SAGESLA_ERR_LAUNCH;
+    }
+    g_wd[dev] = static_cast<int*>(wd);
   }
   return SAGESLA_OK;
 }
@@ -350,6 +361,134 @@ int check_gemm(const void* xq, const float* sx, const void* wq, const float* sw,
   return SAGESLA_OK;
 }
 
+// ---------------------------------------- rows of d channels with strides
+int sm_count(int dev) {
+  int sms = 148;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+// Element strides (batch, token, head) of rows that are read and written in
+// 16-byte pieces.  The stride of an extent of one is never used and reads 0.
+int row_strides(const int64_t* s, int B, int N, int H, int elem_bytes, long out[3]) {
+  const int ext[3] = {B, N, H};
+  for (int i = 0; i < 3; ++i) {
+    out[i] = ext[i] > 1 ? (long)s[i] : 0;
+    if (out[i] < 0 || out[i] >= (1L << 40)) return SAGESLA_ERR_INVALID;
+    if (out[i] * elem_bytes % 16 != 0) return SAGESLA_ERR_MISALIGNED;
+  }
+  return SAGESLA_OK;
+}
+
+// Whether the rows of an output are apart: along the extents above one, from
+// the smallest stride up, each stride passes all that the smaller ones span.
+bool apart(const long s[3], int B, int N, int H, int d) {
+  const int ext[3] = {B, N, H};
+  int order[3] = {0, 1, 2};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (s[order[j]] < s[order[i]]) std::swap(order[i], order[j]);
+  long span = d;
+  for (int i = 0; i < 3; ++i) {
+    const int e = order[i];
+    if (ext[e] == 1) continue;
+    if (s[e] < span) return false;
+    span += s[e] * (ext[e] - 1);
+  }
+  return true;
+}
+
+int rope_common(RopeArgs* a, const void* gamma_q, const void* gamma_k, float eps, const float* cos, const float* sin,
+                const int32_t* pos, int dtype, int B, int N, int Hq, int Hk, int d, int rot, int T, int interleaved) {
+  if (!gamma_q || (Hk && !gamma_k) || !(eps >= 0.f) || eps > 1.f) return SAGESLA_ERR_INVALID;
+  if (dtype != SAGESLA_BF16 && dtype != SAGESLA_FP16 && dtype != SAGESLA_FP32) return SAGESLA_ERR_INVALID;
+  if (interleaved != 0 && interleaved != 1) return SAGESLA_ERR_INVALID;
+  if (B < 1 || N < 1 || (long long)B * N > INT32_MAX || Hq < 1 || Hk < 0 || Hq > 65535 || Hk > 65535)
+    return SAGESLA_ERR_INVALID;
+  if ((double)B * N * ((double)Hq + Hk) >= 8589934592.0) return SAGESLA_ERR_INVALID;
+  if (d < 16 || d > 256 || d % 16 != 0 || rot < 0 || rot > d || rot % 16 != 0) return SAGESLA_ERR_INVALID;
+  if (T < 1 || (rot && (!cos || !sin)) || (!pos && N > T)) return SAGESLA_ERR_INVALID;
+  if (!aligned16(gamma_q) || !aligned16(gamma_k) || !aligned16(cos) || !aligned16(sin) ||
+      (reinterpret_cast<uintptr_t>(pos) & 3u))
+    return SAGESLA_ERR_MISALIGNED;
+  a->t[0].gamma = gamma_q;
+  a->t[0].H = Hq;
+  a->t[1].gamma = gamma_k;
+  a->t[1].H = Hk;
+  a->cos = cos;
+  a->sin = sin;
+  a->pos = pos;
+  a->tokens = (long)B * N;
+  a->N = N;
+  a->T = T;
+  a->d = d;
+  a->rot = rot;
+  a->eps = eps;
+  return SAGESLA_OK;
+}
+
+int rope_rows(RopeTensor* t, const void* x, const void* dy, void* y, const int64_t* xs, const int64_t* dys,
+              const int64_t* ys, int dtype, int B, int N, int d) {
+  const int es = dtype == SAGESLA_FP32 ? 4 : 2;
+  if (!x || !y) return SAGESLA_ERR_INVALID;
+  if (!aligned16(x) || !aligned16(dy) || !aligned16(y)) return SAGESLA_ERR_MISALIGNED;
+  t->x = x;
+  t->dy = dy;
+  t->y = y;
+  SAGESLA_TRY(row_strides(xs, B, N, t->H, es, t->xs));
+  if (dys) SAGESLA_TRY(row_strides(dys, B, N, t->H, es, t->dys));
+  SAGESLA_TRY(row_strides(ys, B, N, t->H, es, t->ys));
+  return apart(t->ys, B, N, t->H, d) ? SAGESLA_OK : SAGESLA_ERR_INVALID;
+}
+
+int decay_common(DecayArgs* a, const void* q, const void* k, const void* v, const float* log_decay,
+                 const float* state_in, float scale, void* out, float* state_out, int B, int N, int H, int Hk, int d) {
+  if (!q || !k || !v || !log_decay || !out || !std::isfinite(scale)) return SAGESLA_ERR_INVALID;
+  if (B < 1 || N < 1 || H < 1 || Hk < 1 || H % Hk != 0 || (d != 64 && d != 128)) return SAGESLA_ERR_INVALID;
+  if ((long long)B * H > 65535 || (double)B * H * N * d >= 1099511627776.0) return SAGESLA_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(state_in) ||
+      !aligned16(state_out) || (reinterpret_cast<uintptr_t>(log_decay) & 3u))
+    return SAGESLA_ERR_MISALIGNED;
+  a->q = static_cast<const uint16_t*>(q);
+  a->k = static_cast<const uint16_t*>(k);
+  a->v = static_cast<const uint16_t*>(v);
+  a->o = static_cast<uint16_t*>(out);
+  a->log_decay = log_decay;
+  a->state_in = state_in;
+  a->state_out = state_out;
+  a->scale = scale;
+  a->B = B;
+  a->N = N;
+  a->H = H;
+  a->Hk = Hk;
+  a->d = d;
+  return SAGESLA_OK;
+}
+
+// ------------------------------------------- W8A8 linear, per token/channel
+constexpr int kTokenMaxK = 131056;  // 2^14 K < 2^31: the INT32 sums are exact
+
+int check_token_rows(int dtype, int rows, int cols, long long ld) {
+  if (dtype != SAGESLA_BF16 && dtype != SAGESLA_FP16) return SAGESLA_ERR_INVALID;
+  if (rows < 1 || cols < 16 || cols % 16 != 0 || cols > kTokenMaxK || (double)rows * cols >= 1099511627776.0)
+    return SAGESLA_ERR_INVALID;
+  if (rows > 1 && (ld < cols || ld >= (1LL << 40))) return SAGESLA_ERR_INVALID;
+  return rows > 1 && ld % 8 != 0 ? SAGESLA_ERR_MISALIGNED : SAGESLA_OK;
+}
+
+int check_token_gemm(const int8_t* wq, const float* sw, const void* bias, const void* y, int dtype, int M, int N,
+                     int K) {
+  if (!wq || !sw || !y || (dtype != SAGESLA_BF16 && dtype != SAGESLA_FP16)) return SAGESLA_ERR_INVALID;
+  if (M < 1 || M > 8388480 || N < 1 || N > 8388480 || K < 16 || K % 16 != 0 || K > kTokenMaxK)
+    return SAGESLA_ERR_INVALID;
+  if ((double)M * N >= 1099511627776.0 || (double)M * K >= 1099511627776.0 || (double)N * K >= 1099511627776.0)
+    return SAGESLA_ERR_INVALID;
+  if (!aligned16(wq) || !aligned16(y) || (reinterpret_cast<uintptr_t>(sw) & 3u) ||
+      (reinterpret_cast<uintptr_t>(bias) & 1u))
+    return SAGESLA_ERR_MISALIGNED;
+  return SAGESLA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -631,6 +770,152 @@ int sagesla_w8a8_linear(const void* x, const void* wq, const float* sw, void* y,
   }
   ProfScope ps(10, st);
   return launch_rc(launch_w8a8_gemm(base, sx, static_cast<const uint8_t*>(wq), sw, y, M, N, K, watchdog(dev), st));
+}
+
+// ------------------------------------------- W8A8 linear, per token/channel
+int sagesla_w8a8_token_quant(const void* a, int dtype, int rows, int cols, long long lda, int8_t* codes, float* scales,
+                             sagesla_stream_t stream) {
+  if (!a || !codes || !scales) return SAGESLA_ERR_INVALID;
+  SAGESLA_TRY(check_token_rows(dtype, rows, cols, lda));
+  if (!aligned16(a) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u)) return SAGESLA_ERR_MISALIGNED;
+  int dev = 0;
+  SAGESLA_TRY(check_device(&dev));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(12, st);
+  return launch_rc(launch_w8a8_token_quant(a, dtype, rows, cols, rows > 1 ? lda : cols, codes, scales, st));
+}
+
+int sagesla_w8a8_token_gemm(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, const void* bias,
+                            void* y, int dtype, int M, int N, int K, sagesla_stream_t stream) {
+  if (!xq || !sx) return SAGESLA_ERR_INVALID;
+  SAGESLA_TRY(check_token_gemm(wq, sw, bias, y, dtype, M, N, K));
+  if (!aligned16(xq) || (reinterpret_cast<uintptr_t>(sx) & 3u)) return SAGESLA_ERR_MISALIGNED;
+  int dev = 0;
+  SAGESLA_TRY(check_device(&dev));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(13, st);
+  return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, watchdog(dev), st));
+}
+
+int sagesla_w8a8_token_workspace(int M, int K, long long* bytes) {
+  if (!bytes || M < 1 || K < 16 || K % 16 != 0 || K > kTokenMaxK) return SAGESLA_ERR_INVALID;
+  *bytes = (long long)(up((size_t)M * K) + up((size_t)M * sizeof(float)));
+  return SAGESLA_OK;
+}
+
+int sagesla_w8a8_token_linear(const void* x, long long ldx, const int8_t* wq, const float* sw, const void* bias,
+                              void* y, int dtype, int M, int N, int K, void* workspace, long long workspace_bytes,
+                              sagesla_stream_t stream) {
+  if (!x || !workspace) return SAGESLA_ERR_INVALID;
+  SAGESLA_TRY(check_token_gemm(wq, sw, bias, y, dtype, M, N, K));
+  SAGESLA_TRY(check_token_rows(dtype, M, K, ldx));
+  long long need = 0;
+  SAGESLA_TRY(sagesla_w8a8_token_workspace(M, K, &need));
+  if (workspace_bytes < need) return SAGESLA_ERR_INVALID;
+  if (!aligned16(x) || !aligned16(workspace)) return SAGESLA_ERR_MISALIGNED;
+  int dev = 0;
+  SAGESLA_TRY(check_device(&dev));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int8_t* xq = static_cast<int8_t*>(workspace);
+  float* sx = reinterpret_cast<float*>(xq + up((size_t)M * K));
+  {
+    ProfScope ps(12, st);
+    SAGESLA_TRY(launch_rc(launch_w8a8_token_quant(x, dtype, M, K, M > 1 ? ldx : K, xq, sx, st)));
+  }
+  ProfScope ps(13, st);
+  return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, watchdog(dev), st));
+}
+
+// ------------------------------------------------- QK norm and rotation
+int sagesla_qk_norm_rope(const void* q, const void* k, const void* gamma_q, const void* gamma_k, float eps,
+                         const float* cos, const float* sin, const int32_t* pos, void* q_out, void* k_out, int dtype,
+                         int B, int N, int Hq, int Hk, int d, int rot, int T, int interleaved,
+                         const int64_t* strides, sagesla_stream_t stream) {
+  RopeArgs a;
+  if (!strides) return SAGESLA_ERR_INVALID;
+  SAGESLA_TRY(rope_common(&a, gamma_q, gamma_k, eps, cos, sin, pos, dtype, B, N, Hq, Hk, d, rot, T, interleaved));
+  SAGESLA_TRY(rope_rows(&a.t[0], q, nullptr, q_out, strides, nullptr, strides + 6, dtype, B, N, d));
+  if (Hk) SAGESLA_TRY(rope_rows(&a.t[1], k, nullptr, k_out, strides + 3, nullptr, strides + 9, dtype, B, N, d));
+  int dev = 0;
+  SAGESLA_TRY(check_device(&dev));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(14, st);
+  return launch_rc(launch_qk_norm_rope(a, dtype, interleaved != 0, false, st));
+}
+
+int sagesla_qk_norm_rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, long long* bytes) {
+  if (!bytes || B < 1 || N < 1 || Hq < 1 || Hk < 0 || d < 16 || d > 256 || (long long)B * N > INT32_MAX || Hq > 65535 ||
+      Hk > 65535)
+    return SAGESLA_ERR_INVALID;
+  int dev = 0;
+  SAGESLA_TRY(check_device(&dev));
+  *bytes = (long long)rope_bwd_workspace(B, N, Hq, Hk, d, sm_count(dev));
+  return SAGESLA_OK;
+}
+
+int sagesla_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                             const void* gamma_q, const void* gamma_k, float eps, const float* cos, const float* sin,
+                             const int32_t* pos, void* dq, void* dk, float* dgamma_q, float* dgamma_k, int dtype,
+                             int B, int N, int Hq, int Hk, int d, int rot, int T, int interleaved,
+                             const int64_t* strides, void* workspace, long long workspace_bytes,
+                             sagesla_stream_t stream) {
+  RopeArgs a;
+  if (!strides || !dq_out || !dgamma_q || !workspace || (Hk && (!dk_out || !dgamma_k))) return SAGESLA_ERR_INVALID;
+  SAGESLA_TRY(rope_common(&a, gamma_q, gamma_k, eps, cos, sin, pos, dtype, B, N, Hq, Hk, d, rot, T, interleaved));
+  SAGESLA_TRY(rope_rows(&a.t[0], q, dq_out, dq, strides + 6, strides, strides + 12, dtype, B, N, d));
+  if (Hk) SAGESLA_TRY(rope_rows(&a.t[1], k, dk_out, dk, strides + 9, strides + 3, strides + 15, dtype, B, N, d));
+  if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(dgamma_q) & 3u) ||
+      (reinterpret_cast<uintptr_t>(dgamma_k) & 3u))
+    return SAGESLA_ERR_MISALIGNED;
+  int dev = 0;
+  SAGESLA_TRY(check_device(&dev));
+  if (workspace_bytes < (long long)rope_bwd_workspace(B, N, Hq, Hk, d, sm_count(dev))) return SAGESLA_ERR_INVALID;
+  a.part = static_cast<float*>(workspace);
+  a.dgq = dgamma_q;
+  a.dgk = Hk ? dgamma_k : nullptr;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(15, st);
+  return launch_rc(launch_qk_norm_rope(a, dtype, interleaved != 0, true, st));
+}
+
+// ------------------------------------------- linear attention with a decay
+int sagesla_linear_decay(const void* q, const void* k, const void* v, const float* log_decay, const float* state_in,
+                         const int32_t* lens, float scale, void* out, float* state_out, int B, int N, int H, int Hk,
+                         int d, const int64_t* strides, sagesla_stream_t stream) {
+  DecayArgs a;
+  if (!strides) return SAGESLA_ERR_INVALID;
+  SAGESLA_TRY(decay_common(&a, q, k, v, log_decay, state_in, scale, out, state_out, B, N, H, Hk, d));
+  if (reinterpret_cast<uintptr_t>(lens) & 3u) return SAGESLA_ERR_MISALIGNED;
+  a.lens = lens;
+  const int nh[4] = {H, Hk, Hk, H};
+  long* to[4] = {a.qs, a.ks, a.vs, a.os};
+  for (int i = 0; i < 4; ++i) SAGESLA_TRY(row_strides(strides + 3 * i, B, N, nh[i], 2, to[i]));
+  if (!apart(a.os, B, N, H, d)) return SAGESLA_ERR_INVALID;
+  int dev = 0;
+  SAGESLA_TRY(check_device(&dev));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(16, st);
+  return launch_rc(launch_linear_decay(a, watchdog(dev), st));
+}
+
+int sagesla_linear_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
+                              const float* state_in, float scale, void* out, float* state_out, int B, int H, int Hk,
+                              int d, const int64_t* strides, sagesla_stream_t stream) {
+  DecayArgs a;
+  if (!strides || !state_out) return SAGESLA_ERR_INVALID;
+  SAGESLA_TRY(decay_common(&a, q, k, v, log_decay, state_in, scale, out, state_out, B, 1, H, Hk, d));
+  const int nh[4] = {H, Hk, Hk, H};
+  long* to[4] = {a.qs, a.ks, a.vs, a.os};
+  for (int i = 0; i < 4; ++i) {
+    const int64_t s[3] = {strides[2 * i], 0, strides[2 * i + 1]};
+    SAGESLA_TRY(row_strides(s, B, 1, nh[i], 2, to[i]));
+  }
+  if (!apart(a.os, B, 1, H, d)) return SAGESLA_ERR_INVALID;
+  int dev = 0;
+  SAGESLA_TRY(check_device(&dev));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(17, st);
+  return launch_rc(launch_linear_decay(a, watchdog(dev), st));
 }
 
 int sagesla_sync_status(sagesla_stream_t stream) {

@@ -89,6 +89,48 @@ size_t w8a8_scales_count(int rows, int cols);
 cudaError_t launch_w8a8_quant(const void* a, int rows, int cols, uint8_t* codes, float* scales, cudaStream_t st);
 cudaError_t launch_w8a8_gemm(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, void* y, int M,
                              int N, int K, int* wd, cudaStream_t st);
+// QK norm and rotation (k_qk_norm_rope.cu): one tensor of the pair.  Strides
+// in elements: batch, token, head.
+struct RopeTensor {
+  const void* x = nullptr;
+  const void* dy = nullptr;  // backward: the gradient of the output
+  void* y = nullptr;         // the output, or dx
+  const void* gamma = nullptr;
+  long xs[3] = {}, dys[3] = {}, ys[3] = {};
+  int H = 0;
+};
+struct RopeArgs {
+  RopeTensor t[2];  // q, k (H = 0: none)
+  const float *cos = nullptr, *sin = nullptr;  // [T][rot/2]
+  const int32_t* pos = nullptr;                // [B][N], or nullptr: the token index
+  float* part = nullptr;                       // backward: a row of q and of k per CTA, [ctas][2][d]
+  float *dgq = nullptr, *dgk = nullptr;
+  long tokens = 0, N = 0, T = 0, stride = 0;
+  int d = 0, rot = 0, L = 0, Gq = 0, G = 0;
+  float eps = 0.f, inv_d = 0.f;
+};
+int rope_bwd_ctas(long tokens, int G, int sms);
+size_t rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, int sms);
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, int dtype, bool interleaved, bool back, cudaStream_t st);
+// W8A8 linear layer with a scale per token and per output channel (k_w8a8_token.cu).
+cudaError_t launch_w8a8_token_quant(const void* a, int dtype, int rows, int cols, long lda, int8_t* codes,
+                                    float* scales, cudaStream_t st);
+cudaError_t launch_w8a8_token_gemm(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                                   const void* bias, void* y, int dtype, int M, int N, int K, int* wd,
+                                   cudaStream_t st);
+// Causal linear attention with a decay for each head (k_linear_decay.cu).
+struct DecayArgs {
+  const uint16_t *q = nullptr, *k = nullptr, *v = nullptr;  // bf16 rows of d
+  uint16_t* o = nullptr;
+  const float* log_decay = nullptr;  // [H]
+  const float* state_in = nullptr;   // [B][H][d][d], or nullptr: zeros
+  float* state_out = nullptr;        // may be state_in; nullptr: not kept
+  const int32_t* lens = nullptr;     // [B], or nullptr: N
+  long qs[3] = {}, ks[3] = {}, vs[3] = {}, os[3] = {};  // strides in elements: batch, token, head
+  float scale = 1.f;
+  int B = 0, N = 0, H = 0, Hk = 0, d = 0;
+};
+cudaError_t launch_linear_decay(const DecayArgs& a, int* wd, cudaStream_t st);
 // Waits `probes` times on an mbarrier that never completes, then sets *wd.
 cudaError_t launch_watchdog_selftest(int probes, int* wd, cudaStream_t st);
 

@@ -794,7 +794,7 @@ int sagesla_w8a8_token_gemm(const int8_t* xq, const float* sx, const int8_t* wq,
   SAGESLA_TRY(check_device(&dev));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(13, st);
-  return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, watchdog(dev), st));
+  return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, watchdog(dev), st, false));
 }
 
 int sagesla_w8a8_token_workspace(int M, int K, long long* bytes) {
@@ -823,7 +823,9 @@ int sagesla_w8a8_token_linear(const void* x, long long ldx, const int8_t* wq, co
     SAGESLA_TRY(launch_rc(launch_w8a8_token_quant(x, dtype, M, K, M > 1 ? ldx : K, xq, sx, st)));
   }
   ProfScope ps(13, st);
-  return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, watchdog(dev), st));
+  // The product may start under the quantiser's end, unless events between
+  // the two are timing them.
+  return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, watchdog(dev), st, !ps.a));
 }
 
 // ------------------------------------------------- QK norm and rotation

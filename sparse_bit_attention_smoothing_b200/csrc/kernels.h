@@ -117,7 +117,7 @@ cudaError_t launch_w8a8_token_quant(const void* a, int dtype, int rows, int cols
                                     float* scales, cudaStream_t st);
 cudaError_t launch_w8a8_token_gemm(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                                    const void* bias, void* y, int dtype, int M, int N, int K, int* wd,
-                                   cudaStream_t st);
+                                   cudaStream_t st, bool chained);  // chained: xq, sx are the previous launch's
 // Causal linear attention with a decay for each head (k_linear_decay.cu).
 struct DecayArgs {
   const uint16_t *q = nullptr, *k = nullptr, *v = nullptr;  // bf16 rows of d

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import inputs  # noqa: F401  (seeded synthetic inputs, no method arithmetic)
 
@@ -295,47 +296,46 @@ def sagesla_w8a8_linear(x, wq, sw, N: int, y=None, stream=None):
 
 # ---- operators of the layer around the attention --------------------------
 # Tensors are checked here (types, shapes, one device), the rest by the
-# library.  Work runs on `stream` (default: the tensors' device's current
-# stream), with that device current for the call; what a call allocates (its
-# outputs and workspace) is allocated on that stream.
-
-def _dtype(t, fp32=False):
-    import torch
-    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2 if fp32 else None}.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{t.dtype} is not supported (bfloat16, float16{', float32' if fp32 else ''})")
-    return code
-
+# library.  Work runs on `stream` (default: the current stream of the tensors'
+# device), with that device current for the call; what a call allocates (its
+# outputs and workspace) is allocated on that stream.  These calls also serve
+# single tokens, whose kernels take a few microseconds, so the checks are
+# written to be cheap.
 
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
-class _On:
-    """The device and stream of a call: `.s` is the stream's handle."""
+def _dtype(t, fp32=False):
+    import torch
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        return 0
+    if dt is torch.float16:
+        return 1
+    if fp32 and dt is torch.float32:
+        return 2
+    raise ValueError(f"{dt} is not supported (bfloat16, float16{', float32' if fp32 else ''})")
 
-    def __init__(self, t, stream, *others):
-        import torch
-        _need(t.is_cuda, "CUDA tensors are needed")
-        for o in others:
-            _need(o is None or o.device == t.device, "the tensors are on different devices")
-        self.ctx = None
-        if stream is not None:
-            _need(stream.device == t.device, "the stream is on another device than the tensors")
-            self.ctx = torch.cuda.stream(stream)  # makes its device current too
-        elif torch.cuda.current_device() != t.device.index:
-            self.ctx = torch.cuda.device(t.device)
-        self.s = (stream if stream is not None else torch.cuda.current_stream(t.device)).cuda_stream
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self
-
-    def __exit__(self, *e):
-        if self.ctx is not None:
-            self.ctx.__exit__(*e)
+def _launch(go, stream, first, *others):
+    """go(stream handle) with the tensors' device and `stream` current."""
+    import torch
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("CUDA tensors are needed")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("the tensors are on different devices")
+    if stream is not None:
+        _need(stream.device.index == dev, "the stream is on another device than the tensors")
+        with torch.cuda.stream(stream):  # makes its device current too
+            return go(stream.cuda_stream)
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return go(torch._C._cuda_getCurrentRawStream(dev))
+    return go(torch._C._cuda_getCurrentRawStream(dev))
 
 
 def _p(t):
@@ -343,8 +343,8 @@ def _p(t):
 
 
 def _vector(t, n, dtype, what):
-    _need(t.dtype == dtype and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
-          f"{what} must be a contiguous {dtype} vector of {n}")
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n}")
 
 
 def sagesla_w8a8_token_quant(a, stream=None):
@@ -353,18 +353,20 @@ def sagesla_w8a8_token_quant(a, stream=None):
     _need(a.dim() == 2 and a.stride(1) == 1, "a must be a matrix with contiguous rows")
     dt = _dtype(a)
     rows, cols = a.shape
-    with _On(a, stream) as on:
-        codes = torch.empty(rows, cols, dtype=torch.int8, device=a.device)
-        scales = torch.empty(rows, dtype=torch.float32, device=a.device)
-        _check(lib().sagesla_w8a8_token_quant(_p(a), dt, rows, cols, a.stride(0), _p(codes), _p(scales), on.s),
-               "sagesla_w8a8_token_quant")
-    return codes, scales
+
+    def go(st):
+        codes = a.new_empty((rows, cols), dtype=torch.int8)
+        scales = a.new_empty((rows,), dtype=torch.float32)
+        _check(lib().sagesla_w8a8_token_quant(a.data_ptr(), dt, rows, cols, a.stride(0), codes.data_ptr(),
+                                              scales.data_ptr(), st), "sagesla_w8a8_token_quant")
+        return codes, scales
+    return _launch(go, stream, a)
 
 
 def _token_weight(wq, sw, bias, K, dtype):
     import torch
-    _need(wq.dim() == 2 and wq.dtype == torch.int8 and wq.is_contiguous() and wq.shape[1] == K,
-          f"wq must be a contiguous int8 [N, {K}] matrix")
+    if wq.dim() != 2 or wq.dtype is not torch.int8 or not wq.is_contiguous() or wq.shape[1] != K:
+        raise ValueError(f"wq must be a contiguous int8 [N, {K}] matrix")
     N = wq.shape[0]
     _vector(sw, N, torch.float32, "sw")
     if bias is not None:
@@ -372,11 +374,10 @@ def _token_weight(wq, sw, bias, K, dtype):
     return N
 
 
-def _token_out(y, M, N, dtype, device):
-    import torch
+def _token_out(y, M, N, dtype, like):
     if y is None:
-        return torch.empty(M, N, dtype=dtype, device=device)
-    _need(y.shape == (M, N) and y.dtype == dtype and y.is_contiguous(), f"y must be a contiguous {dtype} [{M}, {N}]")
+        return like.new_empty((M, N), dtype=dtype)
+    _need(y.shape == (M, N) and y.dtype is dtype and y.is_contiguous(), f"y must be a contiguous {dtype} [{M}, {N}]")
     return y
 
 
@@ -385,15 +386,17 @@ def sagesla_w8a8_token_gemm(xq, sx, wq, sw, bias=None, dtype=None, y=None, strea
     [M] and [N]."""
     import torch
     dtype = dtype or (y.dtype if y is not None else torch.bfloat16)
-    _need(xq.dim() == 2 and xq.dtype == torch.int8 and xq.is_contiguous(), "xq must be a contiguous int8 [M, K] matrix")
+    _need(xq.dim() == 2 and xq.dtype is torch.int8 and xq.is_contiguous(), "xq must be a contiguous int8 [M, K] matrix")
     M, K = xq.shape
     _vector(sx, M, torch.float32, "sx")
     N = _token_weight(wq, sw, bias, K, dtype)
-    with _On(xq, stream, sx, wq, sw, bias, y) as on:
-        y = _token_out(y, M, N, dtype, xq.device)
-        _check(lib().sagesla_w8a8_token_gemm(_p(xq), _p(sx), _p(wq), _p(sw), _p(bias), _p(y), _dtype(y), M, N, K, on.s),
-               "sagesla_w8a8_token_gemm")
-    return y
+
+    def go(st):
+        out = _token_out(y, M, N, dtype, xq)
+        _check(lib().sagesla_w8a8_token_gemm(xq.data_ptr(), sx.data_ptr(), wq.data_ptr(), sw.data_ptr(), _p(bias),
+                                             out.data_ptr(), _dtype(out), M, N, K, st), "sagesla_w8a8_token_gemm")
+        return out
+    return _launch(go, stream, xq, sx, wq, sw, bias, y)
 
 
 def sagesla_w8a8_token_workspace(M: int, K: int) -> int:
@@ -411,53 +414,58 @@ def sagesla_w8a8_token_linear(x, wq, sw, bias=None, y=None, stream=None):
     dt = _dtype(x)
     M, K = x.shape
     N = _token_weight(wq, sw, bias, K, x.dtype)
-    with _On(x, stream, wq, sw, bias, y) as on:
-        y = _token_out(y, M, N, x.dtype, x.device)
+
+    def go(st):
+        out = _token_out(y, M, N, x.dtype, x)
         nb = sagesla_w8a8_token_workspace(M, K)
-        ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
-        _check(lib().sagesla_w8a8_token_linear(_p(x), x.stride(0), _p(wq), _p(sw), _p(bias), _p(y), dt, M, N, K,
-                                               _p(ws), nb, on.s), "sagesla_w8a8_token_linear")
-    return y
+        ws = x.new_empty((nb,), dtype=torch.uint8)
+        _check(lib().sagesla_w8a8_token_linear(x.data_ptr(), x.stride(0), wq.data_ptr(), sw.data_ptr(), _p(bias),
+                                               out.data_ptr(), dt, M, N, K, ws.data_ptr(), nb, st),
+               "sagesla_w8a8_token_linear")
+        return out
+    return _launch(go, stream, x, wq, sw, bias, y)
 
 
 def _rows4(t, B, N, d, dtype, what):
-    _need(t.dim() == 4 and t.shape[0] == B and t.shape[1] == N and t.shape[3] == d and t.dtype == dtype
-          and t.stride(3) == 1, f"{what} must be a {dtype} [{B}, {N}, heads, {d}] tensor with contiguous channels")
-    return t.shape[2]
+    s = t.shape
+    if len(s) != 4 or s[0] != B or s[1] != N or s[3] != d or t.dtype is not dtype or t.stride(3) != 1:
+        raise ValueError(f"{what} must be a {dtype} [{B}, {N}, heads, {d}] tensor with contiguous channels")
+    return s[2]
 
 
 def _strides(*ts):
-    s = [v for t in ts for v in (t.stride()[:3] if t is not None else (0, 0, 0))]
-    return (ctypes.c_int64 * len(s))(*s)
+    """The host array of batch, token, head strides of the tensors (zeros for None)."""
+    s = []
+    for t in ts:
+        s += t.stride()[:3] if t is not None else (0, 0, 0)
+    return struct.pack(f"{len(s)}q", *s)
 
 
 def _rope_args(q, k, gamma_q, gamma_k, cos, sin, pos):
     """(B, N, Hq, Hk, d, rot, T) of the checked tensors of a norm-and-rotation call."""
     import torch
-    _need(q.dim() == 4, "q must be [B, N, H, d]")
+    _need(q.dim() == 4 and q.stride(3) == 1, "q must be a [B, N, H, d] tensor with contiguous channels")
     B, N, Hq, d = q.shape
-    _rows4(q, B, N, d, q.dtype, "q")
-    Hk = 0 if k is None else _rows4(k, B, N, d, q.dtype, "k")
-    _vector(gamma_q, d, q.dtype, "gamma_q")
+    dt = q.dtype
+    Hk = 0 if k is None else _rows4(k, B, N, d, dt, "k")
+    _vector(gamma_q, d, dt, "gamma_q")
     if k is not None:
         _need(gamma_k is not None, "k needs gamma_k")
-        _vector(gamma_k, d, q.dtype, "gamma_k")
-    _need(cos.dim() == 2 and cos.shape == sin.shape and cos.dtype == sin.dtype == torch.float32
-          and cos.is_contiguous() and sin.is_contiguous(), "cos and sin must be contiguous fp32 [T, rot/2] tables")
-    if pos is not None:
-        _need(pos.dtype == torch.int32 and pos.shape == (B, N) and pos.is_contiguous(),
-              f"pos must be a contiguous int32 [{B}, {N}] tensor")
-    return B, N, Hq, Hk, d, 2 * cos.shape[1], cos.shape[0]
+        _vector(gamma_k, d, dt, "gamma_k")
+    T, half = cos.shape if cos.dim() == 2 else (0, -1)
+    if half < 0 or sin.shape != cos.shape or cos.dtype is not torch.float32 or sin.dtype is not torch.float32 \
+            or not cos.is_contiguous() or not sin.is_contiguous():
+        raise ValueError("cos and sin must be contiguous fp32 [T, rot/2] tables")
+    if pos is not None and (pos.dtype is not torch.int32 or pos.shape != (B, N) or not pos.is_contiguous()):
+        raise ValueError(f"pos must be a contiguous int32 [{B}, {N}] tensor")
+    return B, N, Hq, Hk, d, 2 * half, T
 
 
 def _rows_out(t, B, N, H, d, like, head_major, what):
-    import torch
     if t is not None:
         _need(_rows4(t, B, N, d, like.dtype, what) == H, f"{what} must have {H} heads")
         return t
-    shape = (B, H, N, d) if head_major else (B, N, H, d)
-    t = torch.empty(shape, dtype=like.dtype, device=like.device)
-    return t.transpose(1, 2) if head_major else t
+    return like.new_empty((B, H, N, d)).transpose(1, 2) if head_major else like.new_empty((B, N, H, d))
 
 
 def sagesla_qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, pos=None, eps: float = 1e-6, interleaved: bool = True,
@@ -468,15 +476,18 @@ def sagesla_qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, pos=None, eps: float 
     int32 [B, N] (None: the token index; negative: padding, outputs 0).  Returns (q_out, k_out), [B, N, H, d], or
     [B, H, N, d] as sagesla_attn takes it with head_major; q_out, k_out: [B, N, H, d] views to write to."""
     B, N, Hq, Hk, d, rot, T = _rope_args(q, k, gamma_q, gamma_k, cos, sin, pos)
-    with _On(q, stream, k, gamma_q, gamma_k, cos, sin, pos, q_out, k_out) as on:
+    dt = _dtype(q, True)
+
+    def go(st):
         qo = _rows_out(q_out, B, N, Hq, d, q, head_major, "q_out")
         ko = None if k is None else _rows_out(k_out, B, N, Hk, d, q, head_major, "k_out")
-        _check(lib().sagesla_qk_norm_rope(_p(q), _p(k), _p(gamma_q), _p(gamma_k), eps, _p(cos), _p(sin), _p(pos), _p(qo),
-                                          _p(ko), _dtype(q, True), B, N, Hq, Hk, d, rot, T, 1 if interleaved else 0,
-                                          _strides(q, k, qo, ko), on.s), "sagesla_qk_norm_rope")
-    if head_major:
-        return qo.transpose(1, 2), None if ko is None else ko.transpose(1, 2)
-    return qo, ko
+        _check(lib().sagesla_qk_norm_rope(q.data_ptr(), _p(k), gamma_q.data_ptr(), _p(gamma_k), eps, cos.data_ptr(),
+                                          sin.data_ptr(), _p(pos), qo.data_ptr(), _p(ko), dt, B, N, Hq, Hk, d, rot, T,
+                                          1 if interleaved else 0, _strides(q, k, qo, ko), st), "sagesla_qk_norm_rope")
+        if head_major:
+            return qo.transpose(1, 2), None if ko is None else ko.transpose(1, 2)
+        return qo, ko
+    return _launch(go, stream, q, k, gamma_q, gamma_k, cos, sin, pos, q_out, k_out)
 
 
 def sagesla_qk_norm_rope_bwd_workspace(B: int, N: int, Hq: int, Hk: int, d: int) -> int:
@@ -493,29 +504,32 @@ def sagesla_qk_norm_rope_bwd(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, p
     outputs.  Returns (dq, dk, dgamma_q, dgamma_k), dq and dk [B, N, H, d] of q's type, dgamma_* fp32 [d]."""
     import torch
     B, N, Hq, Hk, d, rot, T = _rope_args(q, k, gamma_q, gamma_k, cos, sin, pos)
+    dt = _dtype(q, True)
     _need(_rows4(dq_out, B, N, d, q.dtype, "dq_out") == Hq, f"dq_out must have {Hq} heads")
     if k is None:
         dk_out = dk = None
     else:
         _need(dk_out is not None and _rows4(dk_out, B, N, d, q.dtype, "dk_out") == Hk, f"dk_out must have {Hk} heads")
-    with _On(q, stream, dq_out, dk_out, k, gamma_q, gamma_k, cos, sin, pos, dq, dk) as on:
-        dq = _rows_out(dq, B, N, Hq, d, q, False, "dq")
-        dk = None if k is None else _rows_out(dk, B, N, Hk, d, q, False, "dk")
-        dg = torch.empty(2, d, dtype=torch.float32, device=q.device)
+
+    def go(st):
+        gq = _rows_out(dq, B, N, Hq, d, q, False, "dq")
+        gk = None if k is None else _rows_out(dk, B, N, Hk, d, q, False, "dk")
+        dg = q.new_empty((2, d), dtype=torch.float32)
         nb = sagesla_qk_norm_rope_bwd_workspace(B, N, Hq, Hk, d)
-        ws = torch.empty(nb, dtype=torch.uint8, device=q.device)
-        _check(lib().sagesla_qk_norm_rope_bwd(_p(dq_out), _p(dk_out), _p(q), _p(k), _p(gamma_q), _p(gamma_k), eps,
-                                              _p(cos), _p(sin), _p(pos), _p(dq), _p(dk), _p(dg[0]), _p(dg[1]),
-                                              _dtype(q, True), B, N, Hq, Hk, d, rot, T, 1 if interleaved else 0,
-                                              _strides(dq_out, dk_out, q, k, dq, dk), _p(ws), nb, on.s),
-               "sagesla_qk_norm_rope_bwd")
-    return dq, dk, dg[0], None if k is None else dg[1]
+        ws = q.new_empty((nb,), dtype=torch.uint8)
+        _check(lib().sagesla_qk_norm_rope_bwd(dq_out.data_ptr(), _p(dk_out), q.data_ptr(), _p(k), gamma_q.data_ptr(),
+                                              _p(gamma_k), eps, cos.data_ptr(), sin.data_ptr(), _p(pos), gq.data_ptr(),
+                                              _p(gk), dg.data_ptr(), dg.data_ptr() + 4 * d, dt, B, N, Hq, Hk, d, rot, T,
+                                              1 if interleaved else 0, _strides(dq_out, dk_out, q, k, gq, gk),
+                                              ws.data_ptr(), nb, st), "sagesla_qk_norm_rope_bwd")
+        return gq, gk, dg[0], None if k is None else dg[1]
+    return _launch(go, stream, q, dq_out, dk_out, k, gamma_q, gamma_k, cos, sin, pos, dq, dk)
 
 
 def _decay_state(t, B, H, d, what):
     import torch
-    _need(t.dtype == torch.float32 and t.shape == (B, H, d, d) and t.is_contiguous(),
-          f"{what} must be a contiguous fp32 [{B}, {H}, {d}, {d}] tensor")
+    if t.dtype is not torch.float32 or t.shape != (B, H, d, d) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous fp32 [{B}, {H}, {d}, {d}] tensor")
 
 
 def sagesla_linear_decay(q, k, v, log_decay, state=None, lens=None, scale: float = 1.0, out=None, state_out=None,
@@ -525,7 +539,7 @@ def sagesla_linear_decay(q, k, v, log_decay, state=None, lens=None, scale: float
     [B, H, d, d] before the first token (None: zeros); lens int32 [B] (None: N; out of later rows is 0).  Returns (out,
     state_out): out [B, N, H, d] ([B, H, N, d] with head_major), the state behind the last tokens."""
     import torch
-    _need(q.dim() == 4 and q.dtype == torch.bfloat16, "q must be a bf16 [B, N, H, d] tensor")
+    _need(q.dim() == 4 and q.dtype is torch.bfloat16, "q must be a bf16 [B, N, H, d] tensor")
     B, N, H, d = q.shape
     _rows4(q, B, N, d, q.dtype, "q")
     Hk = _rows4(k, B, N, d, q.dtype, "k")
@@ -535,40 +549,47 @@ def sagesla_linear_decay(q, k, v, log_decay, state=None, lens=None, scale: float
         _decay_state(state, B, H, d, "state")
     if lens is not None:
         _vector(lens, B, torch.int32, "lens")
-    with _On(q, stream, k, v, log_decay, state, lens, out, state_out) as on:
-        o = _rows_out(out, B, N, H, d, q, head_major, "out")
-        if state_out is None:
-            state_out = torch.empty(B, H, d, d, dtype=torch.float32, device=q.device)
+    if state_out is not None:
         _decay_state(state_out, B, H, d, "state_out")
-        _check(lib().sagesla_linear_decay(_p(q), _p(k), _p(v), _p(log_decay), _p(state), _p(lens), scale, _p(o),
-                                          _p(state_out), B, N, H, Hk, d, _strides(q, k, v, o), on.s),
-               "sagesla_linear_decay")
-    return (o.transpose(1, 2) if head_major else o), state_out
+
+    def go(st):
+        o = _rows_out(out, B, N, H, d, q, head_major, "out")
+        so = q.new_empty((B, H, d, d), dtype=torch.float32) if state_out is None else state_out
+        _check(lib().sagesla_linear_decay(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(state),
+                                          _p(lens), scale, o.data_ptr(), so.data_ptr(), B, N, H, Hk, d,
+                                          _strides(q, k, v, o), st), "sagesla_linear_decay")
+        return (o.transpose(1, 2) if head_major else o), so
+    return _launch(go, stream, q, k, v, log_decay, state, lens, out, state_out)
 
 
 def sagesla_linear_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, state_out=None, stream=None):
     """One token of sagesla_linear_decay: q [B, H, d], k, v [B, Hk, d] bf16; state fp32 [B, H, d, d] is updated in
     place unless state_out is given.  Returns (out [B, H, d], the new state)."""
     import torch
-    _need(q.dim() == 3 and q.dtype == torch.bfloat16 and q.stride(2) == 1, "q must be a bf16 [B, H, d] tensor")
+    bf16 = torch.bfloat16
+    _need(q.dim() == 3 and q.dtype is bf16 and q.stride(2) == 1, "q must be a bf16 [B, H, d] tensor")
     B, H, d = q.shape
+    Hk = k.shape[1] if k.dim() == 3 else 0
     for t, what in ((k, "k"), (v, "v")):
-        _need(t.dim() == 3 and t.dtype == torch.bfloat16 and t.shape[0] == B and t.shape[2] == d and t.stride(2) == 1
-              and t.shape[1] == k.shape[1], f"{what} must be a bf16 [{B}, Hk, {d}] tensor")
+        if t.shape != (B, Hk, d) or t.dtype is not bf16 or t.stride(2) != 1:
+            raise ValueError(f"{what} must be a bf16 [{B}, Hk, {d}] tensor")
     _vector(log_decay, H, torch.float32, "log_decay")
     _decay_state(state, B, H, d, "state")
-    with _On(q, stream, k, v, log_decay, state, out, state_out) as on:
-        if out is None:
-            out = torch.empty(B, H, d, dtype=torch.bfloat16, device=q.device)
-        _need(out.shape == q.shape and out.dtype == torch.bfloat16 and out.stride(2) == 1, "out must be like q")
-        if state_out is None:
-            state_out = state
+    if state_out is None:
+        state_out = state
+    else:
         _decay_state(state_out, B, H, d, "state_out")
-        s = [x for t in (q, k, v, out) for x in t.stride()[:2]]
-        _check(lib().sagesla_linear_decay_step(_p(q), _p(k), _p(v), _p(log_decay), _p(state), scale, _p(out),
-                                               _p(state_out), B, H, k.shape[1], d, (ctypes.c_int64 * 8)(*s), on.s),
-               "sagesla_linear_decay_step")
-    return out, state_out
+    if out is not None:
+        _need(out.shape == q.shape and out.dtype is bf16 and out.stride(2) == 1, "out must be like q")
+
+    def go(st):
+        o = q.new_empty((B, H, d)) if out is None else out
+        s = struct.pack("8q", *q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2])
+        _check(lib().sagesla_linear_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                               state.data_ptr(), scale, o.data_ptr(), state_out.data_ptr(), B, H, Hk, d,
+                                               s, st), "sagesla_linear_decay_step")
+        return o, state_out
+    return _launch(go, stream, q, k, v, log_decay, state, out, state_out)
 
 
 def sync_status(stream=None) -> int:

@@ -32,6 +32,7 @@ std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;     // path workspace
 std::map<std::pair<int, cudaStream_t>, Workspace> g_stage;  // host entry point's device staging
 std::map<int, int*> g_wd;        // per-device watchdog word
 std::map<int, int> g_dev_ok;     // per-device: 1 = sm_100, 0 = not
+std::map<int, int> g_sms;        // per-device: SMs
 
 // The watchdog word is static device storage (zero when the library is
 // loaded), so that finding it allocates nothing and is allowed while a stream
@@ -363,8 +364,9 @@ int check_gemm(const void* xq, const float* sx, const void* wq, const float* sw,
 
 // ---------------------------------------- rows of d channels with strides
 int sm_count(int dev) {
-  int sms = 148;
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  std::lock_guard<std::mutex> lk(g_mu);
+  int& sms = g_sms[dev];
+  if (!sms && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 148;
   return sms;
 }
 
@@ -794,7 +796,7 @@ int sagesla_w8a8_token_gemm(const int8_t* xq, const float* sx, const int8_t* wq,
   SAGESLA_TRY(check_device(&dev));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(13, st);
-  return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, watchdog(dev), st, false));
+  return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, sm_count(dev), watchdog(dev), st, false));
 }
 
 int sagesla_w8a8_token_workspace(int M, int K, long long* bytes) {
@@ -825,7 +827,7 @@ int sagesla_w8a8_token_linear(const void* x, long long ldx, const int8_t* wq, co
   ProfScope ps(13, st);
   // The product may start under the quantiser's end, unless events between
   // the two are timing them.
-  return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, watchdog(dev), st, !ps.a));
+  return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, sm_count(dev), watchdog(dev), st, !ps.a));
 }
 
 // ------------------------------------------------- QK norm and rotation
@@ -842,7 +844,7 @@ int sagesla_qk_norm_rope(const void* q, const void* k, const void* gamma_q, cons
   SAGESLA_TRY(check_device(&dev));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(14, st);
-  return launch_rc(launch_qk_norm_rope(a, dtype, interleaved != 0, false, st));
+  return launch_rc(launch_qk_norm_rope(a, dtype, interleaved != 0, false, sm_count(dev), st));
 }
 
 int sagesla_qk_norm_rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, long long* bytes) {
@@ -877,7 +879,7 @@ int sagesla_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void*
   a.dgk = Hk ? dgamma_k : nullptr;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(15, st);
-  return launch_rc(launch_qk_norm_rope(a, dtype, interleaved != 0, true, st));
+  return launch_rc(launch_qk_norm_rope(a, dtype, interleaved != 0, true, sm_count(dev), st));
 }
 
 // ------------------------------------------- linear attention with a decay

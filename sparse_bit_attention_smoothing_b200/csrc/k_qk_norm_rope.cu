@@ -358,14 +358,12 @@ size_t rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, int sms) {
   return (size_t)rope_bwd_ctas((long)B * N, Hq + Hk, sms) * 2 * d * sizeof(float);
 }
 
-cudaError_t launch_qk_norm_rope(const RopeArgs& a0, int dtype, bool interleaved, bool back, cudaStream_t st) {
+cudaError_t launch_qk_norm_rope(const RopeArgs& a0, int dtype, bool interleaved, bool back, int sms,
+                                cudaStream_t st) {
   RopeArgs a = a0;
   a.L = 2;
   while (8 * a.L < a.d) a.L <<= 1;
   a.inv_d = 1.f / (float)a.d;
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (dtype == 0)
     return interleaved ? rope_launch<__nv_bfloat16, true>(a, back, sms, st)
                        : rope_launch<__nv_bfloat16, false>(a, back, sms, st);

@@ -623,11 +623,8 @@ cudaError_t launch_w8a8_token_quant(const void* a, int dtype, int rows, int cols
 }
 
 cudaError_t launch_w8a8_token_gemm(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
-                                   const void* bias, void* y, int dtype, int M, int N, int K, int* wd,
+                                   const void* bias, void* y, int dtype, int M, int N, int K, int sms, int* wd,
                                    cudaStream_t st, bool chained) {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // Few tokens, us with this kernel and with the pairs' (N = K = 5120): 1 token
   // 9.2 and 20, 64 tokens 11.7 and 13.9, 128 tokens 14.2 and 14.0 (N = 13824:
   // 21.9 and 19.1).

@@ -111,12 +111,13 @@ struct RopeArgs {
 };
 int rope_bwd_ctas(long tokens, int G, int sms);
 size_t rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, int sms);
-cudaError_t launch_qk_norm_rope(const RopeArgs& a, int dtype, bool interleaved, bool back, cudaStream_t st);
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, int dtype, bool interleaved, bool back, int sms,
+                                cudaStream_t st);
 // W8A8 linear layer with a scale per token and per output channel (k_w8a8_token.cu).
 cudaError_t launch_w8a8_token_quant(const void* a, int dtype, int rows, int cols, long lda, int8_t* codes,
                                     float* scales, cudaStream_t st);
 cudaError_t launch_w8a8_token_gemm(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
-                                   const void* bias, void* y, int dtype, int M, int N, int K, int* wd,
+                                   const void* bias, void* y, int dtype, int M, int N, int K, int sms, int* wd,
                                    cudaStream_t st, bool chained);  // chained: xq, sx are the previous launch's
 // Causal linear attention with a decay for each head (k_linear_decay.cu).
 struct DecayArgs {

@@ -391,17 +391,26 @@ int sagesla_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void*
  *   state_out the same shape: S behind each sequence's last token (may be
  *            state_in); NULL: not kept.
  *   lens     int32 [B] device: tokens of each sequence (taken into [0, N]);
- *            NULL: N.  Rows at and past the length are not read and their
- *            out is 0; a length of 0 leaves the state as it was.
- * sagesla_linear_decay_step: one token of each sequence (N = 1); strides is a
- *   host array of 8: batch, head of q, k, v, out.
+ *            NULL: N.  Rows at and past the length count for nothing, whatever
+ *            they hold, and their out is 0; a length of 0 leaves the state as
+ *            it was.
+ *   workspace  the bytes that sagesla_linear_decay_workspace tells for the
+ *            current device (0: none, may be NULL), 16-byte aligned, the
+ *            call's own until it has run.
+ *   A v that is not finite makes its channel NaN from its token on, in out
+ *   and in the state; an infinite state, score or k may come out as NaN.
+ * sagesla_linear_decay_step: one token of each sequence (N = 1); state_in and
+ *   state_out are needed (the same for an update in place); strides is a host
+ *   array of 8: batch, head of q, k, v, out.
  * d 64 or 128; Hk divides H; B*H <= 65535.  Pointers 16-byte aligned, strides
- * multiples of 8 elements and not negative, the rows of out apart; out
- * overlaps no input.  Codes as sagesla_attn.
+ * multiples of 8 elements and not negative (between tokens not 0), the rows of
+ * out apart; out overlaps no input.  N <= 2^30.  Codes as sagesla_attn.
  */
+int sagesla_linear_decay_workspace(int B, int N, int H, int d, long long* bytes);
 int sagesla_linear_decay(const void* q, const void* k, const void* v, const float* log_decay, const float* state_in,
                          const int32_t* lens, float scale, void* out, float* state_out, int B, int N, int H, int Hk,
-                         int d, const int64_t* strides, sagesla_stream_t stream);
+                         int d, const int64_t* strides, void* workspace, long long workspace_bytes,
+                         sagesla_stream_t stream);
 int sagesla_linear_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
                               const float* state_in, float scale, void* out, float* state_out, int B, int H, int Hk,
                               int d, const int64_t* strides, sagesla_stream_t stream);

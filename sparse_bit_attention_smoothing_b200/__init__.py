@@ -34,7 +34,7 @@ EXPORTS = ["sagesla_attn", "sagesla_attn_opts", "sagesla_attn_qknorm", "sagesla_
            "sagesla_debug_flash_stall", "sagesla_w8a8_quant", "sagesla_w8a8_gemm", "sagesla_w8a8_linear",
            "sagesla_w8a8_token_quant", "sagesla_w8a8_token_gemm", "sagesla_w8a8_token_workspace",
            "sagesla_w8a8_token_linear", "sagesla_qk_norm_rope", "sagesla_qk_norm_rope_bwd",
-           "sagesla_qk_norm_rope_bwd_workspace", "sagesla_linear_decay", "sagesla_linear_decay_step"]
+           "sagesla_qk_norm_rope_bwd_workspace", "sagesla_linear_decay", "sagesla_linear_decay_workspace", "sagesla_linear_decay_step"]
 KERNELS = ["stats", "stats_final", "quant", "pool_topk", "linear_kv", "linear_sum", "flash", "w_tile",
            "linear_apply", "w8a8_quant", "w8a8_gemm", "rms_inv", "w8a8_token_quant", "w8a8_token_gemm",
            "qk_norm_rope", "qk_norm_rope_bwd", "linear_decay", "linear_decay_step"]
@@ -72,7 +72,8 @@ def lib():
         L.sagesla_qk_norm_rope.argtypes = [P, P, P, P, f, P, P, P, P, P, i, i, i, i, i, i, i, i, i, P, P]
         L.sagesla_qk_norm_rope_bwd_workspace.argtypes = [i, i, i, i, i, P]
         L.sagesla_qk_norm_rope_bwd.argtypes = [P, P, P, P, P, P, f, P, P, P, P, P, P, P, i, i, i, i, i, i, i, i, i, P, P, ll, P]
-        L.sagesla_linear_decay.argtypes = [P, P, P, P, P, P, f, P, P, i, i, i, i, i, P, P]
+        L.sagesla_linear_decay.argtypes = [P, P, P, P, P, P, f, P, P, i, i, i, i, i, P, P, ll, P]
+        L.sagesla_linear_decay_workspace.argtypes = [i, i, i, i, P]
         L.sagesla_linear_decay_step.argtypes = [P, P, P, P, P, f, P, P, i, i, i, i, P, P]
         L.sagesla_strerror.restype = ctypes.c_char_p
         L.sagesla_strerror.argtypes = [i]
@@ -532,6 +533,13 @@ def _decay_state(t, B, H, d, what):
         raise ValueError(f"{what} must be a contiguous fp32 [{B}, {H}, {d}, {d}] tensor")
 
 
+def sagesla_linear_decay_workspace(B: int, N: int, H: int, d: int) -> int:
+    """Bytes of workspace that one sagesla_linear_decay call uses on the current device (0: none)."""
+    n = ctypes.c_longlong(0)
+    _check(lib().sagesla_linear_decay_workspace(B, N, H, d, ctypes.byref(n)), "sagesla_linear_decay_workspace")
+    return n.value
+
+
 def sagesla_linear_decay(q, k, v, log_decay, state=None, lens=None, scale: float = 1.0, out=None, state_out=None,
                          head_major: bool = False, stream=None):
     """Causal linear attention with a decay for each head over whole prompts: S = e^log_decay S + k v^T, out =
@@ -555,9 +563,11 @@ def sagesla_linear_decay(q, k, v, log_decay, state=None, lens=None, scale: float
     def go(st):
         o = _rows_out(out, B, N, H, d, q, head_major, "out")
         so = q.new_empty((B, H, d, d), dtype=torch.float32) if state_out is None else state_out
+        nb = sagesla_linear_decay_workspace(B, N, H, d)
+        ws = q.new_empty((nb,), dtype=torch.uint8) if nb else None
         _check(lib().sagesla_linear_decay(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(state),
                                           _p(lens), scale, o.data_ptr(), so.data_ptr(), B, N, H, Hk, d,
-                                          _strides(q, k, v, o), st), "sagesla_linear_decay")
+                                          _strides(q, k, v, o), _p(ws), nb, st), "sagesla_linear_decay")
         return (o.transpose(1, 2) if head_major else o), so
     return _launch(go, stream, q, k, v, log_decay, state, lens, out, state_out)
 

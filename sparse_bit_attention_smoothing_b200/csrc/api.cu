@@ -446,7 +446,8 @@ int rope_rows(RopeTensor* t, const void* x, const void* dy, void* y, const int64
 int decay_common(DecayArgs* a, const void* q, const void* k, const void* v, const float* log_decay,
                  const float* state_in, float scale, void* out, float* state_out, int B, int N, int H, int Hk, int d) {
   if (!q || !k || !v || !log_decay || !out || !std::isfinite(scale)) return SAGESLA_ERR_INVALID;
-  if (B < 1 || N < 1 || H < 1 || Hk < 1 || H % Hk != 0 || (d != 64 && d != 128)) return SAGESLA_ERR_INVALID;
+  if (B < 1 || N < 1 || N > (1 << 30) || H < 1 || Hk < 1 || H % Hk != 0 || (d != 64 && d != 128))
+    return SAGESLA_ERR_INVALID;
   if ((long long)B * H > 65535 || (double)B * H * N * d >= 1099511627776.0) return SAGESLA_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(state_in) ||
       !aligned16(state_out) || (reinterpret_cast<uintptr_t>(log_decay) & 3u))
@@ -883,9 +884,19 @@ int sagesla_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void*
 }
 
 // ------------------------------------------- linear attention with a decay
+int sagesla_linear_decay_workspace(int B, int N, int H, int d, long long* bytes) {
+  if (!bytes || B < 1 || N < 1 || H < 1 || (long long)B * H > 65535 || (d != 64 && d != 128)) return SAGESLA_ERR_INVALID;
+  int dev = 0;
+  SAGESLA_TRY(check_device(&dev));
+  const int nseg = linear_decay_segments(B, N, H, sm_count(dev));
+  *bytes = nseg > 1 ? (long long)B * H * nseg * d * d * (long long)sizeof(float) : 0;
+  return SAGESLA_OK;
+}
+
 int sagesla_linear_decay(const void* q, const void* k, const void* v, const float* log_decay, const float* state_in,
                          const int32_t* lens, float scale, void* out, float* state_out, int B, int N, int H, int Hk,
-                         int d, const int64_t* strides, sagesla_stream_t stream) {
+                         int d, const int64_t* strides, void* workspace, long long workspace_bytes,
+                         sagesla_stream_t stream) {
   DecayArgs a;
   if (!strides) return SAGESLA_ERR_INVALID;
   SAGESLA_TRY(decay_common(&a, q, k, v, log_decay, state_in, scale, out, state_out, B, N, H, Hk, d));
@@ -893,10 +904,19 @@ int sagesla_linear_decay(const void* q, const void* k, const void* v, const floa
   a.lens = lens;
   const int nh[4] = {H, Hk, Hk, H};
   long* to[4] = {a.qs, a.ks, a.vs, a.os};
-  for (int i = 0; i < 4; ++i) SAGESLA_TRY(row_strides(strides + 3 * i, B, N, nh[i], 2, to[i]));
+  for (int i = 0; i < 4; ++i) {
+    SAGESLA_TRY(row_strides(strides + 3 * i, B, N, nh[i], 2, to[i]));
+    if (N > 1 && to[i][1] == 0) return SAGESLA_ERR_INVALID;
+  }
   if (!apart(a.os, B, N, H, d)) return SAGESLA_ERR_INVALID;
   int dev = 0;
   SAGESLA_TRY(check_device(&dev));
+  long long need = 0;
+  SAGESLA_TRY(sagesla_linear_decay_workspace(B, N, H, d, &need));
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SAGESLA_ERR_INVALID;
+  if (!aligned16(workspace)) return SAGESLA_ERR_MISALIGNED;
+  a.ws = static_cast<float*>(workspace);
+  a.nseg = linear_decay_segments(B, N, H, sm_count(dev));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(16, st);
   return launch_rc(launch_linear_decay(a, watchdog(dev), st));
@@ -906,7 +926,7 @@ int sagesla_linear_decay_step(const void* q, const void* k, const void* v, const
                               const float* state_in, float scale, void* out, float* state_out, int B, int H, int Hk,
                               int d, const int64_t* strides, sagesla_stream_t stream) {
   DecayArgs a;
-  if (!strides || !state_out) return SAGESLA_ERR_INVALID;
+  if (!strides || !state_in || !state_out) return SAGESLA_ERR_INVALID;
   SAGESLA_TRY(decay_common(&a, q, k, v, log_decay, state_in, scale, out, state_out, B, 1, H, Hk, d));
   const int nh[4] = {H, Hk, Hk, H};
   long* to[4] = {a.qs, a.ks, a.vs, a.os};
@@ -919,7 +939,7 @@ int sagesla_linear_decay_step(const void* q, const void* k, const void* v, const
   SAGESLA_TRY(check_device(&dev));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(17, st);
-  return launch_rc(launch_linear_decay(a, watchdog(dev), st));
+  return launch_rc(launch_linear_decay_step(a, sm_count(dev), st));
 }
 
 int sagesla_sync_status(sagesla_stream_t stream) {

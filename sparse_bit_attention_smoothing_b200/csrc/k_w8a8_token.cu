@@ -7,11 +7,11 @@
 // The scales leave the sum over K, so the product runs through the whole of K
 // in INT32 (exact for K <= 131056: 2^14 K < 2^31) and the scales, the bias
 // and the one rounding are the epilogue of the output tile.
-#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tensormap.h"
 
 namespace sagesla {
 
@@ -507,29 +507,11 @@ __global__ void __launch_bounds__(kGemmThreads)
 
 namespace {
 
-using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
-
-EncodeTiled encode_tiled() {
-  static const EncodeTiled f = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
-  return f;
-}
-
 // A row-major [rows][cols] matrix, boxes of bc columns x br rows.
 bool matrix_map(CUtensorMap* m, const void* p, bool half, long rows, long cols, int bc, int br, CUtensorMapSwizzle sw) {
-  const EncodeTiled f = encode_tiled();
-  if (!f) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)cols * (half ? 2 : 1)};
-  const cuuint32_t box[2] = {(cuuint32_t)bc, (cuuint32_t)br}, one[2] = {1, 1};
-  return f(m, half ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims,
-           strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const unsigned long dims[2] = {(unsigned long)cols, (unsigned long)rows}, stride = (unsigned long)cols * (half ? 2 : 1);
+  const unsigned box[2] = {(unsigned)bc, (unsigned)br};
+  return tensor_map(m, p, half ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, dims, &stride, box, sw);
 }
 
 // Cluster of `ctas` CTAs, and the programmatic launch behind the quantiser.

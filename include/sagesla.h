@@ -348,10 +348,10 @@ int sagesla_w8a8_token_linear(const void* x, long long ldx, const int8_t* wq, co
  *   cos, sin fp32 [T][rot/2] device; unused for rot = 0.
  *   pos      int32 [B][N] device: a position of each token, or NULL: the
  *            token's index n (then N <= T).  A token with pos < 0 is padding:
- *            it is not read and its outputs are 0.  pos >= T: its outputs are
+ *            its rows may hold anything and its outputs are 0.  pos >= T: its outputs are
  *            NaN (the tables are not read out of range).
  * d a multiple of 16 from 16 to 256, rot a multiple of 16 from 0 to d; eps in
- * [0, 1]; B*N < 2^31, Hq, Hk <= 65535, B*N*(Hq+Hk) < 2^33.  Pointers 16-byte
+ * [0, 1]; B*N < 2^31, Hq, Hk <= 65535, B*N*(Hq+Hk) < 2^32.  Pointers 16-byte
  * aligned, strides multiples of 16 bytes and not negative; the rows of an
  * output must not overlap.  |x| below 2^60 (squares are summed in fp32).
  * Nothing is allocated: the call can be captured.  Codes as sagesla_attn.

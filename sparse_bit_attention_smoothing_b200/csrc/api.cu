@@ -407,7 +407,7 @@ int rope_common(RopeArgs* a, const void* gamma_q, const void* gamma_k, float eps
   if (interleaved != 0 && interleaved != 1) return SAGESLA_ERR_INVALID;
   if (B < 1 || N < 1 || (long long)B * N > INT32_MAX || Hq < 1 || Hk < 0 || Hq > 65535 || Hk > 65535)
     return SAGESLA_ERR_INVALID;
-  if ((double)B * N * ((double)Hq + Hk) >= 8589934592.0) return SAGESLA_ERR_INVALID;
+  if ((double)B * N * ((double)Hq + Hk) >= 4294967296.0) return SAGESLA_ERR_INVALID;
   if (d < 16 || d > 256 || d % 16 != 0 || rot < 0 || rot > d || rot % 16 != 0) return SAGESLA_ERR_INVALID;
   if (T < 1 || (rot && (!cos || !sin)) || (!pos && N > T)) return SAGESLA_ERR_INVALID;
   if (!aligned16(gamma_q) || !aligned16(gamma_k) || !aligned16(cos) || !aligned16(sin) ||

@@ -104,15 +104,56 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
   for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = r.v[i];
 }
 
-// The lane's part of the token's cos/sin row.  Interleaved pairs: channels
-// 8c .. 8c+7 are pairs 4c .. 4c+3 (four values of each).  Halves: channel j
-// of the first half pairs with j + rot/2, both with value j (eight of each).
+// Eight channels as four packed pairs of fp32 (one instruction for two).
+// Interleaved pairs: e[0], e[1] hold the first and second channels of pairs 0
+// and 1, e[2], e[3] those of pairs 2 and 3.  Halves: channels in order.
+struct Row {
+  uint64_t e[4];
+};
+template <bool kIl>
+__device__ __forceinline__ Row row_of(const float (&f)[8]) {
+  Row r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r.e[i] = kIl ? f32x2_pack(f[4 * (i / 2) + (i & 1)], f[4 * (i / 2) + (i & 1) + 2]) : f32x2_pack(f[2 * i], f[2 * i + 1]);
+  return r;
+}
+template <bool kIl>
+__device__ __forceinline__ void row_to(const Row& r, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (kIl)
+      f32x2_unpack(r.e[i], f[4 * (i / 2) + (i & 1)], f[4 * (i / 2) + (i & 1) + 2]);
+    else
+      f32x2_unpack(r.e[i], f[2 * i], f[2 * i + 1]);
+}
+template <bool kIl, typename T>
+__device__ __forceinline__ Row widen_row(const Piece<T>& p) {
+  float f[8];
+  widen(p, f);
+  return row_of<kIl>(f);
+}
+__device__ __forceinline__ uint64_t neg2(uint64_t v) { return v ^ 0x8000000080000000ull; }
+__device__ __forceinline__ uint64_t both(float v) { return f32x2_pack(v, v); }
+__device__ __forceinline__ float add_halves(uint64_t v) {
+  float a, b;
+  f32x2_unpack(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ float dot_row(const Row& a, const Row& b) {
+  return add_halves(f32x2_fma(a.e[0], b.e[0], f32x2_fma(a.e[1], b.e[1], f32x2_fma(a.e[2], b.e[2], f32x2_mul(a.e[3], b.e[3])))));
+}
+
+// The lane's part of the token's rotation: y = own * c + other * s, where
+// `other` is the pair's other channel.  Interleaved: c and s have a value a
+// pair, in the order of Row's first and second channels (s of the first ones
+// negative).  Halves: a value a channel (s negative in the first half), the
+// other channel in the lane `peer` of the row's group.
 template <bool kIl>
 struct Turn {
-  float c[kIl ? 4 : 8], s[kIl ? 4 : 8];
-  bool on;      // the lane's channels turn
-  bool second;  // (halves) the lane's channels are the second of their pairs
-  int peer;     // (halves) the lane of the row's group that holds the other ones
+  Row c, s;
+  bool on;   // the lane's channels turn
+  int peer;
 };
 template <bool kIl>
 __device__ __forceinline__ Turn<kIl> load_turn(const float* __restrict__ ct, const float* __restrict__ stb, long p,
@@ -120,170 +161,215 @@ __device__ __forceinline__ Turn<kIl> load_turn(const float* __restrict__ ct, con
   Turn<kIl> t;
   const int half = rot / 2;
   t.on = 8 * sub < rot;
-  t.second = false;
   t.peer = sub;
-  constexpr int kNv = kIl ? 1 : 2;
-  int at = 4 * sub;
-  if (!kIl) {
-    t.second = 8 * sub >= half;
-    at = t.second ? 8 * sub - half : 8 * sub;
-    if (t.on) t.peer = t.second ? sub - half / 8 : sub + half / 8;
-  }
-#pragma unroll
-  for (int i = 0; i < kNv; ++i) {
+  float c[8], s[8];
+  if (kIl) {
     float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t.on) {
-      a = __ldg(reinterpret_cast<const float4*>(ct + p * half + at) + i);
-      b = __ldg(reinterpret_cast<const float4*>(stb + p * half + at) + i);
+      a = __ldg(reinterpret_cast<const float4*>(ct + p * half + 4 * sub));
+      b = __ldg(reinterpret_cast<const float4*>(stb + p * half + 4 * sub));
     }
-    t.c[4 * i] = a.x, t.c[4 * i + 1] = a.y, t.c[4 * i + 2] = a.z, t.c[4 * i + 3] = a.w;
-    t.s[4 * i] = b.x, t.s[4 * i + 1] = b.y, t.s[4 * i + 2] = b.z, t.s[4 * i + 3] = b.w;
+    const float cc[4] = {a.x, a.y, a.z, a.w}, ss[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[2 * i] = c[2 * i + 1] = cc[i], s[2 * i] = -ss[i], s[2 * i + 1] = ss[i];
+  } else {
+    const bool second = 8 * sub >= half;
+    const int at = second ? 8 * sub - half : 8 * sub;
+    if (t.on) t.peer = second ? sub - half / 8 : sub + half / 8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t.on) {
+        a = __ldg(reinterpret_cast<const float4*>(ct + p * half + at) + i);
+        b = __ldg(reinterpret_cast<const float4*>(stb + p * half + at) + i);
+      }
+      const float sg = second ? 1.f : -1.f;
+      c[4 * i] = a.x, c[4 * i + 1] = a.y, c[4 * i + 2] = a.z, c[4 * i + 3] = a.w;
+      s[4 * i] = sg * b.x, s[4 * i + 1] = sg * b.y, s[4 * i + 2] = sg * b.z, s[4 * i + 3] = sg * b.w;
+    }
   }
+  t.c = row_of<kIl>(c);
+  t.s = row_of<kIl>(s);
   return t;
 }
-// f <- R f (dir = 1) or R^T f (dir = -1), the lanes of a row together.
+// The other channels of the lane's pairs.
 template <bool kIl>
-__device__ __forceinline__ void turn(float (&f)[8], const Turn<kIl>& t, float dir, int L) {
+__device__ __forceinline__ Row others(const Row& x, int peer, int L) {
+  Row r;
   if (kIl) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = f[2 * i], b = f[2 * i + 1], s = dir * t.s[i];
-      if (t.on) {
-        f[2 * i] = a * t.c[i] - b * s;
-        f[2 * i + 1] = a * s + b * t.c[i];
-      }
-    }
+    r.e[0] = x.e[1], r.e[1] = x.e[0], r.e[2] = x.e[3], r.e[3] = x.e[2];
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(0xffffffffu, f[i], t.peer, L);
-      const float s = t.second ? dir * t.s[i] : -dir * t.s[i];
-      if (t.on) f[i] = f[i] * t.c[i] + o * s;
+    for (int i = 0; i < 4; ++i) r.e[i] = __shfl_sync(0xffffffffu, x.e[i], peer, L);
+  }
+  return r;
+}
+// The same of pieces as stored (halves: half the shuffles of a 16-bit type's).
+template <bool kIl, typename T>
+__device__ __forceinline__ Row other_piece(const Piece<T>& p, const Row& x, int peer, int L) {
+  if constexpr (kIl) {
+    return others<true>(x, peer, L);
+  } else {
+    Piece<T> o;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      o.v[i].x = __shfl_sync(0xffffffffu, p.v[i].x, peer, L);
+      o.v[i].y = __shfl_sync(0xffffffffu, p.v[i].y, peer, L);
+      o.v[i].z = __shfl_sync(0xffffffffu, p.v[i].z, peer, L);
+      o.v[i].w = __shfl_sync(0xffffffffu, p.v[i].w, peer, L);
     }
+    return widen_row<kIl>(o);
   }
 }
 __device__ __forceinline__ float row_sum(float v, int L) {
   for (int o = L >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// 1 / sqrt(mean + eps); NaN for a position outside the tables.
+__device__ __forceinline__ float inv_rms(float ss, const RopeArgs& a, bool far) {
+  return far ? __int_as_float(0x7fffffff) : rsqrtf(ss * a.inv_d + a.eps);
+}
+
+// A head group of a tensor: `pass` passes of R = 32/L heads; the lane's first
+// head is h0, and it has `heads` of the passes' heads.
+struct Group {
+  int tsr, h0, sub, heads;
+  __device__ __forceinline__ Group(const RopeArgs& a, unsigned g) {
+    const int lane = threadIdx.x & 31, R = 32 / a.L;
+    tsr = g >= (unsigned)a.Gq;
+    const int grp = (int)g - (tsr ? a.Gq : 0), pass = a.pass[tsr], H = a.t[tsr].H;
+    sub = lane & (a.L - 1);
+    h0 = grp * R * pass + lane / a.L;
+    heads = h0 < H ? min(pass, (H - 1 - h0) / R + 1) : 0;
+  }
+};
+// Rows of up to U heads: their loads are all on their way before the first is used.
+template <typename T, int U>
+struct Rows {
+  Piece<T> v[U];
+  __device__ __forceinline__ void load(const T* p, long step, int heads) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = u < heads ? load8(p + u * step) : zero8<T>();
+  }
+};
 
 }  // namespace
 
 // ----------------------------------------------------------------- forward --
-// Warp w of the grid: token w / G, head group w % G (the Gq groups of q, then
-// k's); a group is U passes of R = 32/L heads.
+// A warp takes one head group of one token (warp w of the grid: token w / G,
+// group w % G; the Gq groups of q come before k's).  Up to eight rows a lane
+// share the token's rotation and the index arithmetic: with four heads a warp
+// and 64-bit divisions the kernel was bound by issue (720p: 622 us); persistent
+// warps with the next token's rows on their way were slower still (771 us,
+// fewer warps).
 template <typename T, bool kIl, int U>
-__global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopeArgs a) {
-  const long w = (long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, L = a.L, R = 32 / L;
-  const long token = w / a.G;
-  if (token >= a.tokens) return;
-  int grp = (int)(w - token * a.G);
-  const int tsr = grp >= a.Gq;
-  if (tsr) grp -= a.Gq;
-  const long b = token / a.N, n = token - b * a.N;
-  const RopeTensor& t = a.t[tsr];
-  const int sub = lane & (L - 1), h0 = grp * R * U + lane / L;
-  const bool mine = 8 * sub < a.d;
-  const T* x = static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[1] + 8 * sub;
-  T* y = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[1] + 8 * sub;
+__global__ void __launch_bounds__(32 * kWarps, 3) qk_norm_rope_kernel(const RopeArgs a) {
+  const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5), token = w / (unsigned)a.G;
+  if (token >= (unsigned)a.tokens) return;
+  const Group gr(a, w - token * (unsigned)a.G);
+  const RopeTensor& t = a.t[gr.tsr];
+  const int L = a.L, sub = gr.sub, pass = a.pass[gr.tsr];
+  const unsigned b = a.tokens == a.N ? 0 : token / (unsigned)a.N, n = token - b * (unsigned)a.N;
+  const int heads = 8 * sub < a.d ? gr.heads : 0;
+  const long xstep = (32 / L) * t.xs[2], ystep = (32 / L) * t.ys[2];
+  Rows<T, U> in;
+  in.load(static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[1] + gr.h0 * t.xs[2] + 8 * sub, xstep, heads);
+  T* y0 = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[1] + gr.h0 * t.ys[2] + 8 * sub;
   const long p = a.pos ? (long)__ldg(a.pos + token) : n;
-  if (p < 0) {  // padding: zeros
-    const float z[8] = {};
-    for (int u = 0; u < U; ++u)
-      if (mine && h0 + u * R < t.H) store8(y + (h0 + u * R) * t.ys[2], z);
-    return;
-  }
-  Piece<T> in[U];
+  const bool pad = p < 0, far = p >= a.T;  // padding: zeros; no such row of the tables: NaN
+  Turn<kIl> tn = load_turn<kIl>(a.cos, a.sin, pad || far ? 0 : p, a.rot, sub);
+  // gamma goes into the rotation once for all of the warp's rows
+  Row gm = {};
+  if (8 * sub < a.d) gm = widen_row<kIl>(load8(static_cast<const T*>(t.gamma) + 8 * sub));
+  const Row go = others<kIl>(gm, tn.peer, L);
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    in[u] = (mine && h0 + u * R < t.H) ? load8(x + (h0 + u * R) * t.xs[2]) : zero8<T>();
-  const bool far = p >= a.T;  // no such row of the tables: NaN
-  float gm[8] = {};
-  if (mine) widen(load8(static_cast<const T*>(t.gamma) + 8 * sub), gm);
-  const Turn<kIl> tn = load_turn<kIl>(a.cos, a.sin, far ? 0 : p, a.rot, sub);
+  for (int i = 0; i < 4; ++i) {
+    tn.c.e[i] = f32x2_mul(tn.c.e[i], gm.e[i]);
+    tn.s.e[i] = f32x2_mul(tn.s.e[i], go.e[i]);
+  }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    float f[8];
-    widen(in[u], f);
-    float ss = 0.f;
+    if (u >= pass) break;
+    const Row f = widen_row<kIl>(in.v[u]);
+    const Row o = other_piece<kIl>(in.v[u], f, tn.peer, L);
+    const uint64_t r = both(inv_rms(row_sum(dot_row(f, f), L), a, far));
+    Row y;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += f[i] * f[i];
-    ss = row_sum(ss, L);
-    const float r = far ? __int_as_float(0x7fffffff) : __frcp_rn(__fsqrt_rn(ss * a.inv_d + a.eps));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = f[i] * r * gm[i];
-    turn<kIl>(f, tn, 1.f, L);
-    if (mine && h0 + u * R < t.H) store8(y + (h0 + u * R) * t.ys[2], f);
+    for (int i = 0; i < 4; ++i) {
+      y.e[i] = f32x2_mul(f.e[i], tn.c.e[i]);
+      if (tn.on) y.e[i] = f32x2_fma(o.e[i], tn.s.e[i], y.e[i]);
+      y.e[i] = f32x2_mul(y.e[i], r);
+    }
+    if (u < heads) {
+      float v[8];
+      if (pad) y = {};
+      row_to<kIl>(y, v);
+      store8(y0 + u * ystep, v);
+    }
   }
 }
 
 // ---------------------------------------------------------------- backward --
-// Persistent: warp w keeps its head group w % G and walks the tokens
-// w / G, w / G + stride, ..., so its lanes hold the running dgamma of their
-// eight channels in fp32 registers.  The sums of a CTA's warps are joined in
-// shared memory in a fixed order and written as one partial row of q and one
-// of k; dgamma_kernel adds the CTAs' rows in fp64, again in a fixed order:
-// no atomics, the same bits every time.
+// Persistent: warp w keeps its head group w % G and walks the tokens w / G,
+// w / G + stride, ..., so its lanes hold the running dgamma of their eight
+// channels in fp32 registers.  The sums of a CTA's warps are joined in shared
+// memory in a fixed order and written as one partial row of q and one of k;
+// dgamma_kernel adds the CTAs' rows in fp64, again in a fixed order: no
+// atomics, the same bits every time.
 template <typename T, bool kIl, int U>
-__global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_bwd_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 3) qk_norm_rope_bwd_kernel(const RopeArgs a) {
   __shared__ float part[kWarps][256];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, L = a.L, R = 32 / L;
-  const long w = (long)blockIdx.x * kWarps + warp;
-  int grp = (int)(w % a.G);
-  const int tsr = grp >= a.Gq;
-  if (tsr) grp -= a.Gq;
-  const RopeTensor& t = a.t[tsr];
-  const int sub = lane & (L - 1), h0 = grp * R * U + lane / L;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, L = a.L;
+  const unsigned w = blockIdx.x * kWarps + warp;
+  const Group grp(a, w % (unsigned)a.G);
+  const RopeTensor& t = a.t[grp.tsr];
+  const int sub = grp.sub, pass = a.pass[grp.tsr];
   const bool mine = 8 * sub < a.d;
-  float gm[8] = {}, acc[8] = {};
-  if (mine) widen(load8(static_cast<const T*>(t.gamma) + 8 * sub), gm);
-  for (long token = w / a.G; token < a.tokens && w / a.G < a.stride; token += a.stride) {
-    const long b = token / a.N, n = token - b * a.N;
-    const T* x = static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[1] + 8 * sub;
-    const T* dy = static_cast<const T*>(t.dy) + b * t.dys[0] + n * t.dys[1] + 8 * sub;
-    T* dx = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[1] + 8 * sub;
+  const int heads = mine ? grp.heads : 0;
+  const long R = 32 / L, xstep = R * t.xs[2], gstep = R * t.dys[2], ystep = R * t.ys[2];
+  Row gm = {}, sums = {};
+  if (mine) gm = widen_row<kIl>(load8(static_cast<const T*>(t.gamma) + 8 * sub));
+  const unsigned first = w / (unsigned)a.G;
+  const bool one = a.tokens == a.N;
+  for (unsigned token = first; token < (unsigned)a.tokens && first < (unsigned)a.stride; token += (unsigned)a.stride) {
+    const unsigned b = one ? 0 : token / (unsigned)a.N, n = token - b * (unsigned)a.N;
+    Rows<T, U> in, gr;
+    in.load(static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[1] + grp.h0 * t.xs[2] + 8 * sub, xstep, heads);
+    gr.load(static_cast<const T*>(t.dy) + b * t.dys[0] + n * t.dys[1] + grp.h0 * t.dys[2] + 8 * sub, gstep, heads);
+    T* dx = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[1] + grp.h0 * t.ys[2] + 8 * sub;
     const long p = a.pos ? (long)__ldg(a.pos + token) : n;
-    if (p < 0) {  // padding: no gradient
-      const float z[8] = {};
-      for (int u = 0; u < U; ++u)
-        if (mine && h0 + u * R < t.H) store8(dx + (h0 + u * R) * t.ys[2], z);
-      continue;
-    }
-    Piece<T> in[U], gr[U];
+    const bool pad = p < 0, far = p >= a.T;  // padding: no gradient
+    const Turn<kIl> tn = load_turn<kIl>(a.cos, a.sin, pad || far ? 0 : p, a.rot, sub);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool ok = mine && h0 + u * R < t.H;
-      in[u] = ok ? load8(x + (h0 + u * R) * t.xs[2]) : zero8<T>();
-      gr[u] = ok ? load8(dy + (h0 + u * R) * t.dys[2]) : zero8<T>();
-    }
-    const bool far = p >= a.T;
-    const Turn<kIl> tn = load_turn<kIl>(a.cos, a.sin, far ? 0 : p, a.rot, sub);
+      if (u >= pass) break;
+      Row f = widen_row<kIl>(in.v[u]);
+      Row g = widen_row<kIl>(gr.v[u]);
+      const Row o = other_piece<kIl>(gr.v[u], g, tn.peer, L);
+      const uint64_t r = both(inv_rms(row_sum(dot_row(f, f), L), a, far));
+      const bool counts = !pad && u < heads;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float f[8], g[8];
-      widen(in[u], f);
-      widen(gr[u], g);
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += f[i] * f[i];
-      ss = row_sum(ss, L);
-      const float r = far ? __int_as_float(0x7fffffff) : __frcp_rn(__fsqrt_rn(ss * a.inv_d + a.eps));
-      turn<kIl>(g, tn, -1.f, L);
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[i] *= r;  // xh
-        const float gx = g[i] * f[i];
-        if (h0 + u * R < t.H) acc[i] += gx;
-        dot += gx * gm[i];
+      for (int i = 0; i < 4; ++i) {
+        g.e[i] = f32x2_mul(g.e[i], tn.c.e[i]);
+        if (tn.on) g.e[i] = f32x2_fma(o.e[i], neg2(tn.s.e[i]), g.e[i]);  // turned back
+        f.e[i] = f32x2_mul(f.e[i], r);                                   // xh
+        if (counts) sums.e[i] = f32x2_fma(g.e[i], f.e[i], sums.e[i]);
+        g.e[i] = f32x2_mul(g.e[i], gm.e[i]);
       }
-      dot = row_sum(dot, L) * a.inv_d;
+      const uint64_t m = both(-row_sum(dot_row(g, f), L) * a.inv_d);
+      if (u < heads) {
+        Row y;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = r * (g[i] * gm[i] - f[i] * dot);
-      if (mine && h0 + u * R < t.H) store8(dx + (h0 + u * R) * t.ys[2], f);
+        for (int i = 0; i < 4; ++i) y.e[i] = f32x2_mul(r, f32x2_fma(f.e[i], m, g.e[i]));
+        if (pad) y = {};
+        float v[8];
+        row_to<kIl>(y, v);
+        store8(dx + u * ystep, v);
+      }
     }
   }
+  float acc[8];
+  row_to<kIl>(sums, acc);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     for (int o = L; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
@@ -320,15 +406,25 @@ __global__ void __launch_bounds__(256) dgamma_kernel(const float* __restrict__ p
 
 namespace {
 
-constexpr int kBwdCtasPerSm = 4;
+constexpr int kCtasPerSm = 3;
 
 template <typename T, bool kIl>
 cudaError_t rope_launch(const RopeArgs& a0, bool back, int sms, cudaStream_t st) {
-  constexpr int U = 4, UB = 2;
+  constexpr int U = sizeof(T) == 4 ? 4 : 8, UB = sizeof(T) == 4 ? 2 : 4;
   RopeArgs a = a0;
-  const int per = (32 / a.L) * (back ? UB : U);
-  a.Gq = (a.t[0].H + per - 1) / per;
-  a.G = a.Gq + (a.t[1].H + per - 1) / per;
+  const int R = 32 / a.L, most = back ? UB : U;
+  // Even groups of at most `most` passes; single ones where the tokens are too
+  // few to give every SM four warps otherwise.
+  const auto groups = [&](int tsr, int cap) {
+    const int passes = (a.t[tsr].H + R - 1) / R, g = (passes + cap - 1) / cap;
+    a.pass[tsr] = g ? (passes + g - 1) / g : 0;
+    return g ? (passes + a.pass[tsr] - 1) / a.pass[tsr] : 0;
+  };
+  for (int cap = most;; cap = 1) {
+    a.Gq = groups(0, cap);
+    a.G = a.Gq + groups(1, cap);
+    if (cap == 1 || a.tokens * a.G >= 4L * sms) break;
+  }
   if (!back) {
     const long ctas = (a.tokens * a.G + kWarps - 1) / kWarps;
     qk_norm_rope_kernel<T, kIl, U><<<(unsigned)ctas, 32 * kWarps, 0, st>>>(a);
@@ -345,10 +441,11 @@ cudaError_t rope_launch(const RopeArgs& a0, bool back, int sms, cudaStream_t st)
 
 }  // namespace
 
-// CTAs of the backward pass: enough for every (token, group) pair or four an SM, and at least one warp a group.
+// CTAs of the backward pass: enough for every (token, group) pair or three an
+// SM, and at least one warp a group.
 int rope_bwd_ctas(long tokens, int G, int sms) {
   const long need = (tokens * G + kWarps - 1) / kWarps;
-  long ctas = need < (long)kBwdCtasPerSm * sms ? need : (long)kBwdCtasPerSm * sms;
+  long ctas = need < (long)kCtasPerSm * sms ? need : (long)kCtasPerSm * sms;
   const long least = ((long)G + kWarps - 1) / kWarps;
   return (int)(ctas > least ? ctas : least);
 }

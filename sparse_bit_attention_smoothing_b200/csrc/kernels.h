@@ -106,7 +106,7 @@ struct RopeArgs {
   float* part = nullptr;                       // backward: a row of q and of k per CTA, [ctas][2][d]
   float *dgq = nullptr, *dgk = nullptr;
   long tokens = 0, N = 0, T = 0, stride = 0;
-  int d = 0, rot = 0, L = 0, Gq = 0, G = 0;
+  int d = 0, rot = 0, L = 0, Gq = 0, G = 0, pass[2] = {};
   float eps = 0.f, inv_d = 0.f;
 };
 int rope_bwd_ctas(long tokens, int G, int sms);

@@ -225,6 +225,45 @@ __device__ __forceinline__ float row_sum(float v, int L) {
   for (int o = L >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// The row sums of U passes at once (U a power of two): in each of the first
+// log2(U) steps a lane gives away half of the values it still holds, so U sums
+// take U - 1 + log2(L) - log2(U) shuffles instead of U log2(L).  The sum of
+// pass u ends in the lanes whose leading bits of `sub` are u's: take() brings
+// it to the others.  Rows of fewer than U lanes take the plain way.
+template <int U>
+struct Sums {
+  float v[U];
+  bool split;
+  __device__ __forceinline__ void reduce(int L, int sub) {
+    split = L >= U;
+    if (!split) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = row_sum(v[u], L);
+      return;
+    }
+    int o = L >> 1;
+#pragma unroll
+    for (int half = U / 2; half > 0; half >>= 1, o >>= 1) {
+      const bool up = sub & o;
+#pragma unroll
+      for (int i = 0; i < half; ++i) {
+        const float give = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+    for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  }
+  template <class F>
+  __device__ __forceinline__ void apply(F f) {  // one evaluation a lane where a lane holds one sum
+    v[0] = f(v[0]);
+    if (!split)
+#pragma unroll
+      for (int u = 1; u < U; ++u) v[u] = f(v[u]);
+  }
+  __device__ __forceinline__ float take(int u, int L) const {
+    return split ? __shfl_sync(0xffffffffu, v[0], u * (L / U), L) : v[u];
+  }
+};
 // 1 / sqrt(mean + eps); NaN for a position outside the tables.
 __device__ __forceinline__ float inv_rms(float ss, const RopeArgs& a, bool far) {
   return far ? __int_as_float(0x7fffffff) : rsqrtf(ss * a.inv_d + a.eps);
@@ -257,13 +296,14 @@ struct Rows {
 
 // ----------------------------------------------------------------- forward --
 // A warp takes one head group of one token (warp w of the grid: token w / G,
-// group w % G; the Gq groups of q come before k's).  Up to eight rows a lane
-// share the token's rotation and the index arithmetic: with four heads a warp
-// and 64-bit divisions the kernel was bound by issue (720p: 622 us); persistent
-// warps with the next token's rows on their way were slower still (771 us,
-// fewer warps).
+// group w % G; the Gq groups of q come before k's).  What it costs beside the
+// bytes is issue slots, so up to eight rows a lane share the token's rotation,
+// the index arithmetic and the reduction.  720p (q, k of 40 heads, 3.1 GB),
+// us: four rows a warp and a reduction for each 622, eight rows 579, one
+// reduction for all 517 (6.1 TB/s); persistent warps with the next token's
+// rows on their way 771 (fewer warps).
 template <typename T, bool kIl, int U>
-__global__ void __launch_bounds__(32 * kWarps, 3) qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, kIl ? 3 : 2) qk_norm_rope_kernel(const RopeArgs a) {
   const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5), token = w / (unsigned)a.G;
   if (token >= (unsigned)a.tokens) return;
   const Group gr(a, w - token * (unsigned)a.G);
@@ -276,8 +316,13 @@ __global__ void __launch_bounds__(32 * kWarps, 3) qk_norm_rope_kernel(const Rope
   in.load(static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[1] + gr.h0 * t.xs[2] + 8 * sub, xstep, heads);
   T* y0 = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[1] + gr.h0 * t.ys[2] + 8 * sub;
   const long p = a.pos ? (long)__ldg(a.pos + token) : n;
-  const bool pad = p < 0, far = p >= a.T;  // padding: zeros; no such row of the tables: NaN
-  Turn<kIl> tn = load_turn<kIl>(a.cos, a.sin, pad || far ? 0 : p, a.rot, sub);
+  if (p < 0) {  // padding: zeros
+    const float z[8] = {};
+    for (int u = 0; u < heads; ++u) store8(y0 + u * ystep, z);
+    return;
+  }
+  const bool far = p >= a.T;  // no such row of the tables: NaN
+  Turn<kIl> tn = load_turn<kIl>(a.cos, a.sin, far ? 0 : p, a.rot, sub);
   // gamma goes into the rotation once for all of the warp's rows
   Row gm = {};
   if (8 * sub < a.d) gm = widen_row<kIl>(load8(static_cast<const T*>(t.gamma) + 8 * sub));
@@ -287,25 +332,36 @@ __global__ void __launch_bounds__(32 * kWarps, 3) qk_norm_rope_kernel(const Rope
     tn.c.e[i] = f32x2_mul(tn.c.e[i], gm.e[i]);
     tn.s.e[i] = f32x2_mul(tn.s.e[i], go.e[i]);
   }
+  Sums<U> r;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    r.v[u] = 0.f;
+    if (u < pass) {
+      const Row f = widen_row<kIl>(in.v[u]);
+      r.v[u] = dot_row(f, f);
+    }
+  }
+  r.reduce(L, sub);
+  r.apply([&](float ss) { return inv_rms(ss, a, far); });
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (u >= pass) break;
     const Row f = widen_row<kIl>(in.v[u]);
     const Row o = other_piece<kIl>(in.v[u], f, tn.peer, L);
-    const uint64_t r = both(inv_rms(row_sum(dot_row(f, f), L), a, far));
+    const uint64_t rr = both(r.take(u, L));
     Row y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       y.e[i] = f32x2_mul(f.e[i], tn.c.e[i]);
       if (tn.on) y.e[i] = f32x2_fma(o.e[i], tn.s.e[i], y.e[i]);
-      y.e[i] = f32x2_mul(y.e[i], r);
+      y.e[i] = f32x2_mul(y.e[i], rr);
     }
     if (u < heads) {
       float v[8];
-      if (pad) y = {};
       row_to<kIl>(y, v);
-      store8(y0 + u * ystep, v);
+      store8(y0, v);
     }
+    y0 += ystep;
   }
 }
 
@@ -317,7 +373,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) qk_norm_rope_kernel(const Rope
 // dgamma_kernel adds the CTAs' rows in fp64, again in a fixed order: no
 // atomics, the same bits every time.
 template <typename T, bool kIl, int U>
-__global__ void __launch_bounds__(32 * kWarps, 3) qk_norm_rope_bwd_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 2) qk_norm_rope_bwd_kernel(const RopeArgs a) {
   __shared__ float part[kWarps][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, L = a.L;
   const unsigned w = blockIdx.x * kWarps + warp;
@@ -338,34 +394,59 @@ __global__ void __launch_bounds__(32 * kWarps, 3) qk_norm_rope_bwd_kernel(const 
     gr.load(static_cast<const T*>(t.dy) + b * t.dys[0] + n * t.dys[1] + grp.h0 * t.dys[2] + 8 * sub, gstep, heads);
     T* dx = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[1] + grp.h0 * t.ys[2] + 8 * sub;
     const long p = a.pos ? (long)__ldg(a.pos + token) : n;
-    const bool pad = p < 0, far = p >= a.T;  // padding: no gradient
-    const Turn<kIl> tn = load_turn<kIl>(a.cos, a.sin, pad || far ? 0 : p, a.rot, sub);
+    if (p < 0) {  // padding: no gradient
+      const float z[8] = {};
+      for (int u = 0; u < heads; ++u) store8(dx + u * ystep, z);
+      continue;
+    }
+    const bool far = p >= a.T;
+    Turn<kIl> tn = load_turn<kIl>(a.cos, a.sin, far ? 0 : p, a.rot, sub);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tn.s.e[i] = neg2(tn.s.e[i]);  // turned back
+    // Both row sums come from x as it is: mean(u xh) = r mean(u x), and
+    //   dx = r u - x r^3 mean(u x).
+    Sums<U> r, m;
+    Row g[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      r.v[u] = m.v[u] = 0.f;
+      g[u] = {};
+      if (u < pass) {
+        const Row f = widen_row<kIl>(in.v[u]), dyr = widen_row<kIl>(gr.v[u]);
+        const Row o = other_piece<kIl>(gr.v[u], dyr, tn.peer, L);
+        Row gm_f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          g[u].e[i] = f32x2_mul(dyr.e[i], tn.c.e[i]);
+          if (tn.on) g[u].e[i] = f32x2_fma(o.e[i], tn.s.e[i], g[u].e[i]);
+          gm_f.e[i] = f32x2_mul(f.e[i], gm.e[i]);
+        }
+        r.v[u] = dot_row(f, f);
+        m.v[u] = dot_row(g[u], gm_f);
+      }
+    }
+    r.reduce(L, sub);
+    m.reduce(L, sub);
+    r.apply([&](float ss) { return inv_rms(ss, a, far); });
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u >= pass) break;
-      Row f = widen_row<kIl>(in.v[u]);
-      Row g = widen_row<kIl>(gr.v[u]);
-      const Row o = other_piece<kIl>(gr.v[u], g, tn.peer, L);
-      const uint64_t r = both(inv_rms(row_sum(dot_row(f, f), L), a, far));
-      const bool counts = !pad && u < heads;
+      const float rv = r.take(u, L);
+      const uint64_t rr = both(rv), k = both(-(rv * (m.take(u, L) * a.inv_d)) * rv * rv);  // in this order: no overflow
+      const Row f = widen_row<kIl>(in.v[u]);
+      Row y;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        g.e[i] = f32x2_mul(g.e[i], tn.c.e[i]);
-        if (tn.on) g.e[i] = f32x2_fma(o.e[i], neg2(tn.s.e[i]), g.e[i]);  // turned back
-        f.e[i] = f32x2_mul(f.e[i], r);                                   // xh
-        if (counts) sums.e[i] = f32x2_fma(g.e[i], f.e[i], sums.e[i]);
-        g.e[i] = f32x2_mul(g.e[i], gm.e[i]);
+        const uint64_t gr2 = f32x2_mul(g[u].e[i], rr);
+        sums.e[i] = f32x2_fma(gr2, f.e[i], sums.e[i]);  // a lane without this head has zeros
+        y.e[i] = f32x2_fma(f.e[i], k, f32x2_mul(gr2, gm.e[i]));
       }
-      const uint64_t m = both(-row_sum(dot_row(g, f), L) * a.inv_d);
       if (u < heads) {
-        Row y;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y.e[i] = f32x2_mul(r, f32x2_fma(f.e[i], m, g.e[i]));
-        if (pad) y = {};
         float v[8];
         row_to<kIl>(y, v);
-        store8(dx + u * ystep, v);
+        store8(dx, v);
       }
+      dx += ystep;
     }
   }
   float acc[8];
@@ -406,7 +487,7 @@ __global__ void __launch_bounds__(256) dgamma_kernel(const float* __restrict__ p
 
 namespace {
 
-constexpr int kCtasPerSm = 3;
+constexpr int kCtasPerSm = 2;
 
 template <typename T, bool kIl>
 cudaError_t rope_launch(const RopeArgs& a0, bool back, int sms, cudaStream_t st) {
@@ -441,7 +522,7 @@ cudaError_t rope_launch(const RopeArgs& a0, bool back, int sms, cudaStream_t st)
 
 }  // namespace
 
-// CTAs of the backward pass: enough for every (token, group) pair or three an
+// CTAs of the backward pass: enough for every (token, group) pair or two an
 // SM, and at least one warp a group.
 int rope_bwd_ctas(long tokens, int G, int sms) {
   const long need = (tokens * G + kWarps - 1) / kWarps;

@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 from . import inputs  # noqa: F401  (seeded synthetic inputs, no method arithmetic)
 
@@ -296,108 +295,52 @@ def sagesla_w8a8_linear(x, wq, sw, N: int, y=None, stream=None):
 
 
 # ---- operators of the layer around the attention --------------------------
-# Tensors are checked here (types, shapes, one device), the rest by the
-# library.  Work runs on `stream` (default: the current stream of the tensors'
-# device), with that device current for the call; what a call allocates (its
-# outputs and workspace) is allocated on that stream.  These calls also serve
-# single tokens, whose kernels take a few microseconds, so the checks are
-# written to be cheap.
-
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+# These serve single tokens too, whose kernels take a few microseconds, so the
+# checks of the tensors (ValueError), the allocations and the call of the C ABI
+# are compiled (csrc/binding.cpp, _layer.so).  Work runs on `stream` (default:
+# the current stream of the tensors' device); what a call allocates (its
+# outputs and workspace) is allocated on that stream.
+_layer_mod = None
 
 
-def _dtype(t, fp32=False):
+def _layer():
+    global _layer_mod
+    if _layer_mod is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries, before the module that links them)
+        lib()
+        path = os.path.join(_HERE, "_layer.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: run `python -m sparse_bit_attention_smoothing_b200.build`")
+        spec = importlib.util.spec_from_file_location("_layer", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _layer_mod = mod
+    return _layer_mod
+
+
+def _on(stream, tensor, f, *args):
+    """f(*args) with `stream` (and its device) current."""
     import torch
-    dt = t.dtype
-    if dt is torch.bfloat16:
-        return 0
-    if dt is torch.float16:
-        return 1
-    if fp32 and dt is torch.float32:
-        return 2
-    raise ValueError(f"{dt} is not supported (bfloat16, float16{', float32' if fp32 else ''})")
-
-
-def _launch(go, stream, first, *others):
-    """go(stream handle) with the tensors' device and `stream` current."""
-    import torch
-    dev = first.get_device()
-    if dev < 0:
-        raise ValueError("CUDA tensors are needed")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("the tensors are on different devices")
-    if stream is not None:
-        _need(stream.device.index == dev, "the stream is on another device than the tensors")
-        with torch.cuda.stream(stream):  # makes its device current too
-            return go(stream.cuda_stream)
-    if torch._C._cuda_getDevice() != dev:
-        with torch.cuda.device(dev):
-            return go(torch._C._cuda_getCurrentRawStream(dev))
-    return go(torch._C._cuda_getCurrentRawStream(dev))
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
-def _vector(t, n, dtype, what):
-    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n}")
+    if stream.device != tensor.device:
+        raise ValueError("the stream is on another device than the tensors")
+    with torch.cuda.stream(stream):
+        return f(*args)
 
 
 def sagesla_w8a8_token_quant(a, stream=None):
     """INT8 codes [rows, cols] (row-major) and fp32 scales [rows] of a bf16 or fp16 CUDA matrix, one scale a row."""
-    import torch
-    _need(a.dim() == 2 and a.stride(1) == 1, "a must be a matrix with contiguous rows")
-    dt = _dtype(a)
-    rows, cols = a.shape
-
-    def go(st):
-        codes = a.new_empty((rows, cols), dtype=torch.int8)
-        scales = a.new_empty((rows,), dtype=torch.float32)
-        _check(lib().sagesla_w8a8_token_quant(a.data_ptr(), dt, rows, cols, a.stride(0), codes.data_ptr(),
-                                              scales.data_ptr(), st), "sagesla_w8a8_token_quant")
-        return codes, scales
-    return _launch(go, stream, a)
-
-
-def _token_weight(wq, sw, bias, K, dtype):
-    import torch
-    if wq.dim() != 2 or wq.dtype is not torch.int8 or not wq.is_contiguous() or wq.shape[1] != K:
-        raise ValueError(f"wq must be a contiguous int8 [N, {K}] matrix")
-    N = wq.shape[0]
-    _vector(sw, N, torch.float32, "sw")
-    if bias is not None:
-        _vector(bias, N, dtype, "bias")
-    return N
-
-
-def _token_out(y, M, N, dtype, like):
-    if y is None:
-        return like.new_empty((M, N), dtype=dtype)
-    _need(y.shape == (M, N) and y.dtype is dtype and y.is_contiguous(), f"y must be a contiguous {dtype} [{M}, {N}]")
-    return y
+    f = _layer().w8a8_token_quant
+    return f(a) if stream is None else _on(stream, a, f, a)
 
 
 def sagesla_w8a8_token_gemm(xq, sx, wq, sw, bias=None, dtype=None, y=None, stream=None):
     """y = (xq . wq^T) sx sw + bias, [M, N] of `dtype` (y's, or bf16): codes int8 [M, K] and [N, K], scales fp32
-    [M] and [N]."""
-    import torch
-    dtype = dtype or (y.dtype if y is not None else torch.bfloat16)
-    _need(xq.dim() == 2 and xq.dtype is torch.int8 and xq.is_contiguous(), "xq must be a contiguous int8 [M, K] matrix")
-    M, K = xq.shape
-    _vector(sx, M, torch.float32, "sx")
-    N = _token_weight(wq, sw, bias, K, dtype)
-
-    def go(st):
-        out = _token_out(y, M, N, dtype, xq)
-        _check(lib().sagesla_w8a8_token_gemm(xq.data_ptr(), sx.data_ptr(), wq.data_ptr(), sw.data_ptr(), _p(bias),
-                                             out.data_ptr(), _dtype(out), M, N, K, st), "sagesla_w8a8_token_gemm")
-        return out
-    return _launch(go, stream, xq, sx, wq, sw, bias, y)
+    [M] and [N], bias [N] of y's type."""
+    f = _layer().w8a8_token_gemm
+    args = (xq, sx, wq, sw, bias, dtype, y)
+    return f(*args) if stream is None else _on(stream, xq, f, *args)
 
 
 def sagesla_w8a8_token_workspace(M: int, K: int) -> int:
@@ -410,63 +353,8 @@ def sagesla_w8a8_token_workspace(M: int, K: int) -> int:
 def sagesla_w8a8_token_linear(x, wq, sw, bias=None, y=None, stream=None):
     """The linear layer in 8-bit integers, a scale per token of x (bf16 or fp16 [M, K]) and per output channel of the
     weight (codes and scales of sagesla_w8a8_token_quant): y [M, N] of x's type."""
-    import torch
-    _need(x.dim() == 2 and x.stride(1) == 1, "x must be a matrix with contiguous rows")
-    dt = _dtype(x)
-    M, K = x.shape
-    N = _token_weight(wq, sw, bias, K, x.dtype)
-
-    def go(st):
-        out = _token_out(y, M, N, x.dtype, x)
-        nb = sagesla_w8a8_token_workspace(M, K)
-        ws = x.new_empty((nb,), dtype=torch.uint8)
-        _check(lib().sagesla_w8a8_token_linear(x.data_ptr(), x.stride(0), wq.data_ptr(), sw.data_ptr(), _p(bias),
-                                               out.data_ptr(), dt, M, N, K, ws.data_ptr(), nb, st),
-               "sagesla_w8a8_token_linear")
-        return out
-    return _launch(go, stream, x, wq, sw, bias, y)
-
-
-def _rows4(t, B, N, d, dtype, what):
-    s = t.shape
-    if len(s) != 4 or s[0] != B or s[1] != N or s[3] != d or t.dtype is not dtype or t.stride(3) != 1:
-        raise ValueError(f"{what} must be a {dtype} [{B}, {N}, heads, {d}] tensor with contiguous channels")
-    return s[2]
-
-
-def _strides(*ts):
-    """The host array of batch, token, head strides of the tensors (zeros for None)."""
-    s = []
-    for t in ts:
-        s += t.stride()[:3] if t is not None else (0, 0, 0)
-    return struct.pack(f"{len(s)}q", *s)
-
-
-def _rope_args(q, k, gamma_q, gamma_k, cos, sin, pos):
-    """(B, N, Hq, Hk, d, rot, T) of the checked tensors of a norm-and-rotation call."""
-    import torch
-    _need(q.dim() == 4 and q.stride(3) == 1, "q must be a [B, N, H, d] tensor with contiguous channels")
-    B, N, Hq, d = q.shape
-    dt = q.dtype
-    Hk = 0 if k is None else _rows4(k, B, N, d, dt, "k")
-    _vector(gamma_q, d, dt, "gamma_q")
-    if k is not None:
-        _need(gamma_k is not None, "k needs gamma_k")
-        _vector(gamma_k, d, dt, "gamma_k")
-    T, half = cos.shape if cos.dim() == 2 else (0, -1)
-    if half < 0 or sin.shape != cos.shape or cos.dtype is not torch.float32 or sin.dtype is not torch.float32 \
-            or not cos.is_contiguous() or not sin.is_contiguous():
-        raise ValueError("cos and sin must be contiguous fp32 [T, rot/2] tables")
-    if pos is not None and (pos.dtype is not torch.int32 or pos.shape != (B, N) or not pos.is_contiguous()):
-        raise ValueError(f"pos must be a contiguous int32 [{B}, {N}] tensor")
-    return B, N, Hq, Hk, d, 2 * half, T
-
-
-def _rows_out(t, B, N, H, d, like, head_major, what):
-    if t is not None:
-        _need(_rows4(t, B, N, d, like.dtype, what) == H, f"{what} must have {H} heads")
-        return t
-    return like.new_empty((B, H, N, d)).transpose(1, 2) if head_major else like.new_empty((B, N, H, d))
+    f = _layer().w8a8_token_linear
+    return f(x, wq, sw, bias, y) if stream is None else _on(stream, x, f, x, wq, sw, bias, y)
 
 
 def sagesla_qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, pos=None, eps: float = 1e-6, interleaved: bool = True,
@@ -476,19 +364,9 @@ def sagesla_qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, pos=None, eps: float 
     cos, sin fp32 [T, rot/2], the first rot channels turned in pairs (2c, 2c+1) (interleaved) or (c, c + rot/2); pos
     int32 [B, N] (None: the token index; negative: padding, outputs 0).  Returns (q_out, k_out), [B, N, H, d], or
     [B, H, N, d] as sagesla_attn takes it with head_major; q_out, k_out: [B, N, H, d] views to write to."""
-    B, N, Hq, Hk, d, rot, T = _rope_args(q, k, gamma_q, gamma_k, cos, sin, pos)
-    dt = _dtype(q, True)
-
-    def go(st):
-        qo = _rows_out(q_out, B, N, Hq, d, q, head_major, "q_out")
-        ko = None if k is None else _rows_out(k_out, B, N, Hk, d, q, head_major, "k_out")
-        _check(lib().sagesla_qk_norm_rope(q.data_ptr(), _p(k), gamma_q.data_ptr(), _p(gamma_k), eps, cos.data_ptr(),
-                                          sin.data_ptr(), _p(pos), qo.data_ptr(), _p(ko), dt, B, N, Hq, Hk, d, rot, T,
-                                          1 if interleaved else 0, _strides(q, k, qo, ko), st), "sagesla_qk_norm_rope")
-        if head_major:
-            return qo.transpose(1, 2), None if ko is None else ko.transpose(1, 2)
-        return qo, ko
-    return _launch(go, stream, q, k, gamma_q, gamma_k, cos, sin, pos, q_out, k_out)
+    f = _layer().qk_norm_rope
+    args = (q, k, gamma_q, gamma_k, cos, sin, pos, eps, interleaved, q_out, k_out, head_major)
+    return f(*args) if stream is None else _on(stream, q, f, *args)
 
 
 def sagesla_qk_norm_rope_bwd_workspace(B: int, N: int, Hq: int, Hk: int, d: int) -> int:
@@ -503,34 +381,9 @@ def sagesla_qk_norm_rope_bwd(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, p
                              interleaved: bool = True, dq=None, dk=None, stream=None):
     """Backward pass of sagesla_qk_norm_rope: dq_out, dk_out [B, N, H, d] (any strides) are the gradients of its
     outputs.  Returns (dq, dk, dgamma_q, dgamma_k), dq and dk [B, N, H, d] of q's type, dgamma_* fp32 [d]."""
-    import torch
-    B, N, Hq, Hk, d, rot, T = _rope_args(q, k, gamma_q, gamma_k, cos, sin, pos)
-    dt = _dtype(q, True)
-    _need(_rows4(dq_out, B, N, d, q.dtype, "dq_out") == Hq, f"dq_out must have {Hq} heads")
-    if k is None:
-        dk_out = dk = None
-    else:
-        _need(dk_out is not None and _rows4(dk_out, B, N, d, q.dtype, "dk_out") == Hk, f"dk_out must have {Hk} heads")
-
-    def go(st):
-        gq = _rows_out(dq, B, N, Hq, d, q, False, "dq")
-        gk = None if k is None else _rows_out(dk, B, N, Hk, d, q, False, "dk")
-        dg = q.new_empty((2, d), dtype=torch.float32)
-        nb = sagesla_qk_norm_rope_bwd_workspace(B, N, Hq, Hk, d)
-        ws = q.new_empty((nb,), dtype=torch.uint8)
-        _check(lib().sagesla_qk_norm_rope_bwd(dq_out.data_ptr(), _p(dk_out), q.data_ptr(), _p(k), gamma_q.data_ptr(),
-                                              _p(gamma_k), eps, cos.data_ptr(), sin.data_ptr(), _p(pos), gq.data_ptr(),
-                                              _p(gk), dg.data_ptr(), dg.data_ptr() + 4 * d, dt, B, N, Hq, Hk, d, rot, T,
-                                              1 if interleaved else 0, _strides(dq_out, dk_out, q, k, gq, gk),
-                                              ws.data_ptr(), nb, st), "sagesla_qk_norm_rope_bwd")
-        return gq, gk, dg[0], None if k is None else dg[1]
-    return _launch(go, stream, q, dq_out, dk_out, k, gamma_q, gamma_k, cos, sin, pos, dq, dk)
-
-
-def _decay_state(t, B, H, d, what):
-    import torch
-    if t.dtype is not torch.float32 or t.shape != (B, H, d, d) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous fp32 [{B}, {H}, {d}, {d}] tensor")
+    f = _layer().qk_norm_rope_bwd
+    args = (dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, pos, eps, interleaved, dq, dk)
+    return f(*args) if stream is None else _on(stream, q, f, *args)
 
 
 def sagesla_linear_decay_workspace(B: int, N: int, H: int, d: int) -> int:
@@ -546,60 +399,17 @@ def sagesla_linear_decay(q, k, v, log_decay, state=None, lens=None, scale: float
     scale q S.  q [B, N, H, d], k, v [B, N, Hk, d] bf16 with any strides; log_decay fp32 [H]; state fp32
     [B, H, d, d] before the first token (None: zeros); lens int32 [B] (None: N; out of later rows is 0).  Returns (out,
     state_out): out [B, N, H, d] ([B, H, N, d] with head_major), the state behind the last tokens."""
-    import torch
-    _need(q.dim() == 4 and q.dtype is torch.bfloat16, "q must be a bf16 [B, N, H, d] tensor")
-    B, N, H, d = q.shape
-    _rows4(q, B, N, d, q.dtype, "q")
-    Hk = _rows4(k, B, N, d, q.dtype, "k")
-    _need(_rows4(v, B, N, d, q.dtype, "v") == Hk, "k and v must have the same heads")
-    _vector(log_decay, H, torch.float32, "log_decay")
-    if state is not None:
-        _decay_state(state, B, H, d, "state")
-    if lens is not None:
-        _vector(lens, B, torch.int32, "lens")
-    if state_out is not None:
-        _decay_state(state_out, B, H, d, "state_out")
-
-    def go(st):
-        o = _rows_out(out, B, N, H, d, q, head_major, "out")
-        so = q.new_empty((B, H, d, d), dtype=torch.float32) if state_out is None else state_out
-        nb = sagesla_linear_decay_workspace(B, N, H, d)
-        ws = q.new_empty((nb,), dtype=torch.uint8) if nb else None
-        _check(lib().sagesla_linear_decay(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(state),
-                                          _p(lens), scale, o.data_ptr(), so.data_ptr(), B, N, H, Hk, d,
-                                          _strides(q, k, v, o), _p(ws), nb, st), "sagesla_linear_decay")
-        return (o.transpose(1, 2) if head_major else o), so
-    return _launch(go, stream, q, k, v, log_decay, state, lens, out, state_out)
+    f = _layer().linear_decay
+    args = (q, k, v, log_decay, state, lens, scale, out, state_out, head_major)
+    return f(*args) if stream is None else _on(stream, q, f, *args)
 
 
 def sagesla_linear_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, state_out=None, stream=None):
     """One token of sagesla_linear_decay: q [B, H, d], k, v [B, Hk, d] bf16; state fp32 [B, H, d, d] is updated in
     place unless state_out is given.  Returns (out [B, H, d], the new state)."""
-    import torch
-    bf16 = torch.bfloat16
-    _need(q.dim() == 3 and q.dtype is bf16 and q.stride(2) == 1, "q must be a bf16 [B, H, d] tensor")
-    B, H, d = q.shape
-    Hk = k.shape[1] if k.dim() == 3 else 0
-    for t, what in ((k, "k"), (v, "v")):
-        if t.shape != (B, Hk, d) or t.dtype is not bf16 or t.stride(2) != 1:
-            raise ValueError(f"{what} must be a bf16 [{B}, Hk, {d}] tensor")
-    _vector(log_decay, H, torch.float32, "log_decay")
-    _decay_state(state, B, H, d, "state")
-    if state_out is None:
-        state_out = state
-    else:
-        _decay_state(state_out, B, H, d, "state_out")
-    if out is not None:
-        _need(out.shape == q.shape and out.dtype is bf16 and out.stride(2) == 1, "out must be like q")
-
-    def go(st):
-        o = q.new_empty((B, H, d)) if out is None else out
-        s = struct.pack("8q", *q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2])
-        _check(lib().sagesla_linear_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                                               state.data_ptr(), scale, o.data_ptr(), state_out.data_ptr(), B, H, Hk, d,
-                                               s, st), "sagesla_linear_decay_step")
-        return o, state_out
-    return _launch(go, stream, q, k, v, log_decay, state, out, state_out)
+    f = _layer().linear_decay_step
+    args = (q, k, v, log_decay, state, scale, out, state_out)
+    return f(*args) if stream is None else _on(stream, q, f, *args)
 
 
 def sync_status(stream=None) -> int:

@@ -15,6 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsagesla.so")
+LAYER = os.path.join(PKG, "_layer.so")  # the compiled part of the Python binding (csrc/binding.cpp)
 SOURCES = ["k_prologue.cu", "k_topk.cu", "k_linear.cu", "k_flash.cu", "k_flash64.cu", "k_watchdog.cu", "k_w8a8.cu", "k_w8a8_token.cu", "k_qk_norm_rope.cu",
            "k_linear_decay.cu", "api.cu", "noalloc.cu"]
 HEADERS = ["common.cuh", "kernels.h", "tensormap.h"]
@@ -63,7 +64,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + ".tmp%d" % os.getpid()
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])
         os.replace(tmp, LIB)
+    build_layer(force)
     return LIB
+
+
+def build_layer(force: bool = False) -> str:
+    """The compiled binding of the layer operators, against the installed torch and libsagesla.so."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and not _stale(LAYER, [src, os.path.join(ROOT, "include", "sagesla.h")]):
+        return LAYER
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+    inc = [f"-I{p}" for p in ext.include_paths("cuda") + [sysconfig.get_paths()["include"]]]
+    libs = [a for p in ext.library_paths("cuda") for a in (f"-L{p}", f"-Wl,-rpath,{p}")]
+    tmp = LAYER + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-DTORCH_EXTENSION_NAME=_layer",
+           "-DTORCH_API_INCLUDE_EXTENSION_H", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, src,
+           "-o", tmp, f"-L{PKG}", "-lsagesla", "-Wl,-rpath,$ORIGIN", *libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+    os.replace(tmp, LAYER)
+    return LAYER
 
 
 if __name__ == "__main__":

@@ -52,8 +52,12 @@ struct Lay {
   static constexpr int pbuf = vpart + 2 * 3 * tile;          // two of P' in two parts
   static constexpr int misc = pbuf + (kOut ? 4 * kBlk : 0);
   static constexpr int bytes = misc + 1536 + 1024;
-  static constexpr int threads = kOut ? 512 : 384;
+  static constexpr int threads = kOut ? 640 : 384;
 };
+// Registers of the walk's five warpgroups (copies and MMAs, state, state, P',
+// outputs): they share what the CTA was launched with, 96 a thread.
+constexpr int kRegs = 96, kRegsIssue = 40, kRegsState = 120, kRegsP = 88, kRegsO = 104;
+static_assert(kRegsIssue + 2 * kRegsState + kRegsP + kRegsO <= 5 * kRegs, "registers");
 constexpr int kAhead = 4;  // chunks that are brought to L2 before their copy to shared memory is issued
 
 __device__ __forceinline__ uint64_t desc_mn(const void* p, uint32_t block_stride) {  // MN-major, 128-byte swizzle
@@ -80,6 +84,14 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, i
       : "memory");
 }
 
+template <int kN>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kN));
+}
+template <int kN>
+__device__ __forceinline__ void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN));
+}
 __device__ __forceinline__ void tma_prefetch_4d(const void* map, int x, int n, int h, int b) {
   asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(x), "r"(n),
                "r"(h), "r"(b)
@@ -100,18 +112,18 @@ __device__ __forceinline__ uint32_t take_part(float& a, float& b) {
 // kOut: the walk over a segment, with outputs.  Otherwise the segment's own
 // state.  One CTA a (segment, head, sequence).  Warps: 0 the copies, 1 the
 // MMAs, 4-11 the state (a channel of v and half of the channels of k a
-// thread) and the parts of v, 12-15 P' and the outputs.
+// thread) and the parts of v, 12-15 P', 16-19 the outputs.
 // kParts of v: three where the state leaves the kernel, two where it only
 // feeds outputs (a walk whose states come from the carried segments).
 template <int D, bool kOut, int kParts>
-__global__ void __launch_bounds__(kOut ? 512 : 384, 1)
+__global__ void __launch_bounds__(kOut ? 640 : 384, 1)
     linear_decay_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                         const __grid_constant__ CUtensorMap mv, const DecayArgs a, int* wd) {
   using L = Lay<D, kOut>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   struct Misc {
-    uint64_t full[L::stages], empty[L::stages], p_full[2], p_empty[2], vp_full[2], u_full, s_full, s_read, pp_full[2], o_full, o_empty, fin;
+    uint64_t full[L::stages], empty[L::stages], p_full[2], p_empty[2], vp_full[2], u_full, s_full, s_read, pp_full[2], pp_empty[2], o_full, o_empty, fin;
     float power[kPowers + 3];   // l^m
     float out_power[kC];        // scale l^{i+1}
     int bad[128];  // per channel of v: the segment's first token that is not finite
@@ -137,6 +149,7 @@ __global__ void __launch_bounds__(kOut ? 512 : 384, 1)
       mbar_init(&ms->p_empty[i], 4);
       mbar_init(&ms->vp_full[i], 8);
       mbar_init(&ms->pp_full[i], 4);
+      mbar_init(&ms->pp_empty[i], 4);
     }
     mbar_init(&ms->u_full, 1);
     mbar_init(&ms->s_full, 8);
@@ -163,6 +176,7 @@ __global__ void __launch_bounds__(kOut ? 512 : 384, 1)
   constexpr int oK = (kOut ? 1 : 0) * L::tile, oV = oK + L::tile;
   bool ok = true;
 
+  if (kOut && warp < 4) regs_fewer<kRegsIssue>();
   if (warp == 0) {
     // ------------------------------- copies -------------------------------
     int c = 0;
@@ -284,6 +298,7 @@ __global__ void __launch_bounds__(kOut ? 512 : 384, 1)
     __syncwarp();
   } else if (warp >= 4 && warp < 12) {
     // ------------------------- the state, parts of v ----------------------
+    if (kOut) regs_more<kRegsState>();
     constexpr int KD = D / 2;               // channels of k of the thread's
     const int ch = 32 * (warp & 3) + lane;  // channel of v
     const int kb = (warp >> 3) * KD;        // first channel of k
@@ -427,17 +442,16 @@ __global__ void __launch_bounds__(kOut ? 512 : 384, 1)
 #pragma unroll
       for (int k = 0; k < KD; ++k) to[(size_t)(kb + k) * D + ch] = nan ? __int_as_float(0x7fffffff) : S[k];
     }
-  } else if (kOut && warp >= 12) {
-    // ----------------------------- P', outputs ----------------------------
+  } else if (kOut && warp >= 12 && warp < 16) {
+    // --------------------------------- P' ---------------------------------
+    regs_fewer<kRegsP>();
     const int q = warp & 3, i = 16 * q + (lane & 15), jb = 32 * (lane >> 4);  // the thread's row and columns of P
-    const int ch = 32 * q + lane;
-    uint16_t* out = a.o + b * a.os[0] + h * a.os[2] + (long)t0 * a.os[1];
     float fac[32];  // scale l^{i-j}: the same in every chunk
 #pragma unroll
     for (int j = 0; j < 32; ++j) fac[j] = a.scale * ms->power[max(i - jb - j, 0)];
-    auto probs = [&](int c) {  // P' of chunk c
+    for (int c = 0; c < nc; ++c) {
       ok = __all_sync(0xffffffffu, mbar_wait(&ms->p_full[c & 1], (c >> 1) & 1, abort, wd));
-      if (!ok) return;
+      if (!ok) break;
       tc_fence_after();
       uint32_t p[32];
       SAGESLA_TMEM_LD2H_X32(tmem + quad + kTP + 64 * (c & 1), 32, p);
@@ -445,6 +459,9 @@ __global__ void __launch_bounds__(kOut ? 512 : 384, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms->p_empty[c & 1]);
+      // the outputs of two chunks ago have left this buffer
+      ok = __all_sync(0xffffffffu, mbar_wait(&ms->pp_empty[c & 1], ((c >> 1) & 1) ^ 1, abort, wd));
+      if (!ok) break;
       uint8_t* pb = smem + L::pbuf + (c & 1) * 2 * kBlk + i * 128;
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
@@ -463,20 +480,22 @@ __global__ void __launch_bounds__(kOut ? 512 : 384, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms->pp_full[c & 1]);
-    };
-    if (nc) probs(0);
-    for (int c = 0; ok && c < nc; ++c) {
-      if (c + 1 < nc) probs(c + 1);
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&ms->o_full, c & 1, abort, wd));
+    }
+  } else if (kOut && warp >= 16) {
+    // ------------------------------- outputs ------------------------------
+    regs_more<kRegsO>();
+    const int q = warp & 3, ch = 32 * q + lane;
+    uint16_t* out = a.o + b * a.os[0] + h * a.os[2] + (long)t0 * a.os[1];
+    for (int c = 0; c < nc; ++c) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&ms->o_full, c & 1, abort, wd));
       if (!ok) break;
       tc_fence_after();
       const int n = min(kC, valid - c * kC);
       if (32 * q < D) {
         // [channel of v][token] from TMEM to rows of 32 channels: 64-byte rows
-        // in shared memory, then 16 bytes a lane.  They lie where the warp's
-        // own 16 rows of this chunk's P' were, which no MMA reads any more:
-        // tokens 0-31 over the first part's rows, 32-63 over the second's.
-        uint8_t* ob = smem + L::pbuf + (c & 1) * 2 * kBlk + q * 2048;
+        // in shared memory, then 16 bytes a lane.  They lie where this chunk's
+        // P' was, which no MMA reads any more.
+        uint8_t* ob = smem + L::pbuf + (c & 1) * 2 * kBlk + q * 4096;
         const int bad = *reinterpret_cast<volatile int*>(&ms->bad[ch]) - c * kC;
 #pragma unroll
         for (int i0 = 0; i0 < kC; i0 += 32) {
@@ -484,7 +503,12 @@ __global__ void __launch_bounds__(kOut ? 512 : 384, 1)
           SAGESLA_TMEM_LD32(tmem + quad + kTOI + i0, oi);
           SAGESLA_TMEM_LD32(tmem + quad + kTOS + i0, os);
           tmem_ld_wait();
-          uint16_t* to = reinterpret_cast<uint16_t*>(ob + (i0 / 32) * kBlk) + lane;
+          if (i0 + 32 == kC) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms->o_empty);
+          }
+          uint16_t* to = reinterpret_cast<uint16_t*>(ob + i0 * 64) + lane;
           if (bad < kC) {
 #pragma unroll
             for (int x = 0; x < 32; ++x)
@@ -500,19 +524,19 @@ __global__ void __launch_bounds__(kOut ? 512 : 384, 1)
             to[(x + 1) * 32] = (uint16_t)(w >> 16);
           }
         }
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->o_empty);
         uint16_t* row = out + (long)(c * kC + (lane >> 2)) * a.os[1] + 32 * q + 8 * (lane & 3);
 #pragma unroll
         for (int i0 = 0; i0 < kC; i0 += 8) {
-          const uint4 w = *reinterpret_cast<const uint4*>(ob + (i0 / 32) * kBlk + (i0 % 32 + (lane >> 2)) * 64 + 16 * (lane & 3));
+          const uint4 w = *reinterpret_cast<const uint4*>(ob + (i0 + (lane >> 2)) * 64 + 16 * (lane & 3));
           if (i0 + (lane >> 2) < n) *reinterpret_cast<uint4*>(row) = w;
           row += 8 * a.os[1];
         }
         __syncwarp();
+        if (lane == 0) mbar_arrive(&ms->pp_empty[c & 1]);
       } else if (lane == 0) {
         mbar_arrive(&ms->o_empty);
+        mbar_arrive(&ms->pp_empty[c & 1]);
       }
     }
     for (int n = valid + q; n < t1 - t0; n += 4)  // rows of padding
@@ -628,6 +652,11 @@ cudaError_t decay_launch(DecayArgs a, int* wd, cudaStream_t st) {
   const auto run = [&](auto* fn, int threads, int bytes) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
+    if (threads == 640) {  // the walk's warpgroups share out exactly these registers: with fewer they would wait for ever
+      cudaFuncAttributes at;
+      if ((e = cudaFuncGetAttributes(&at, fn)) != cudaSuccess) return e;
+      if (at.numRegs < kRegs) return cudaErrorInvalidKernelImage;
+    }
     fn<<<grid, threads, bytes, st>>>(mq, mk, mv, a, wd);
     return cudaGetLastError();
   };

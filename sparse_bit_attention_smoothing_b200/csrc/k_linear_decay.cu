@@ -35,29 +35,35 @@ constexpr int kC = 64;            // tokens of a chunk
 constexpr int kBlk = kC * 128;    // 64 tokens x 64 channels of bf16: rows of 128 bytes, 128-byte swizzle
 constexpr int kPowers = kC + 1;
 
-// TMEM columns.
-constexpr uint32_t kTP = 0;      // P, two buffers of 64 (64 rows: lanes 0-15 of each quadrant)
-constexpr uint32_t kTOI = 128;   // sum_j v_j P'_ij  [channels of v][i]
-constexpr uint32_t kTOS = 192;   // S^T q_i          [channels of v][i]
-constexpr uint32_t kTU = 256;    // the chunk's own state [channels of v][channels of k]
+// TMEM columns.  v parts: l^{n-1-j} v_j [channels of v][two tokens a column],
+// 32 columns a part.
+constexpr uint32_t kTP = 0;      // walk: P (64 rows: lanes 0-15 of each quadrant)
+constexpr uint32_t kTOI = 128;   //       sum_j v_j P'_ij  [channels of v][i]
+constexpr uint32_t kTOS = 192;   //       S^T q_i          [channels of v][i]
 constexpr uint32_t kTSH = 384, kTSL = 448;  // S^T in two bf16 parts, two channels of k a column
+template <bool kOut>
+__device__ __forceinline__ uint32_t vp_col(int c) { return kOut ? 64 : (c & 1) * 96; }
+template <bool kOut>
+__device__ __forceinline__ uint32_t u_col(int c) { return kOut ? 256 : 256 + (c & 1) * 128; }  // [channels of v][of k]
 
 template <int D, bool kOut>
 struct Lay {
   static constexpr int tile = D / 64 * kBlk;                 // one tensor's chunk
   static constexpr int tensors = kOut ? 3 : 2;               // (q), k, v
-  static constexpr int stages = D == 128 && kOut ? 2 : 3;
+  static constexpr int stages = kOut ? 3 : 5;
   static constexpr int stage = tensors * tile;
-  static constexpr int vpart = stages * stage;               // two buffers of the parts of l^{n-1-j} v_j
-  static constexpr int pbuf = vpart + 2 * 3 * tile;          // two of P' in two parts
+  static constexpr int third = stages * stage;               // walk: the third part of v [tokens][channels]
+  static constexpr int pbuf = third + (kOut ? tile : 0);     // two of P' in two parts
   static constexpr int misc = pbuf + (kOut ? 4 * kBlk : 0);
-  static constexpr int bytes = misc + 1536 + 1024;
-  static constexpr int threads = kOut ? 640 : 384;
+  static constexpr int bytes = misc + 2048 + 1024;
 };
-// Registers of the walk's five warpgroups (copies and MMAs, state, state, P',
-// outputs): they share what the CTA was launched with, 96 a thread.
-constexpr int kRegs = 96, kRegsIssue = 40, kRegsState = 120, kRegsP = 88, kRegsO = 104;
-static_assert(kRegsIssue + 2 * kRegsState + kRegsP + kRegsO <= 5 * kRegs, "registers");
+constexpr int kThreads = 640;
+// Registers of the five warpgroups (copies and MMAs; state, state; and in the
+// walk operands, outputs, otherwise operands twice): they share what the CTA
+// was launched with, 96 a thread.
+constexpr int kRegs = 96, kRegsIssue = 48, kRegsState = 112, kRegsOperands = 104, kRegsOut = 104, kRegsParts = 104;
+static_assert(kRegsIssue + 2 * kRegsState + kRegsOperands + kRegsOut <= 5 * kRegs, "registers");
+static_assert(kRegsIssue + 2 * kRegsState + 2 * kRegsParts <= 5 * kRegs, "registers");
 constexpr int kAhead = 4;  // chunks that are brought to L2 before their copy to shared memory is issued
 
 __device__ __forceinline__ uint64_t desc_mn(const void* p, uint32_t block_stride) {  // MN-major, 128-byte swizzle
@@ -98,6 +104,36 @@ __device__ __forceinline__ void tma_prefetch_4d(const void* map, int x, int n, i
                : "memory");
 }
 
+// 16 lanes in fragments of 8 x 8 16-bit matrices.  Store: register 2k holds,
+// of lane t/4, column 4k + t%4, register 2k + 1 the same of lane t/4 + 8.
+__device__ __forceinline__ void tmem_st_16x128b(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+// Load: registers 4k, 4k + 1 hold, of lane t/4, columns 8k + 2 (t%4) and the
+// next, registers 4k + 2, 4k + 3 the same of lane t/4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+// Four 8 x 8 matrices of 16-bit values, transposed on the way.
+__device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stsm_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
 // Two values in bf16 parts, packed (a low, b high); `a`, `b` become what is left.
 __device__ __forceinline__ uint32_t take_part(float& a, float& b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -112,25 +148,31 @@ __device__ __forceinline__ uint32_t take_part(float& a, float& b) {
 // kOut: the walk over a segment, with outputs.  Otherwise the segment's own
 // state.  One CTA a (segment, head, sequence).  Warps: 0 the copies, 1 the
 // MMAs, 4-11 the state (a channel of v and half of the channels of k a
-// thread) and the parts of v, 12-15 P', 16-19 the outputs.
+// thread), 12-15 the parts of v and P' (a segment's own state: the parts of
+// every second chunk), 16-19 the outputs (the parts of the other chunks).
 // kParts of v: three where the state leaves the kernel, two where it only
 // feeds outputs (a walk whose states come from the carried segments).
+//
+// What the design turns on is shared memory's bandwidth: the walk's MMAs read
+// 100 KB of it a chunk with the parts of v in TMEM, 170 KB with them in shared
+// memory (and two chunks' copies fit then, not three).
 template <int D, bool kOut, int kParts>
-__global__ void __launch_bounds__(kOut ? 640 : 384, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     linear_decay_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                         const __grid_constant__ CUtensorMap mv, const DecayArgs a, int* wd) {
   using L = Lay<D, kOut>;
+  constexpr int NB = kOut ? 1 : 2;  // buffers of the parts of v and of the chunk's own state
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   struct Misc {
-    uint64_t full[L::stages], empty[L::stages], p_full[2], p_empty[2], vp_full[2], u_full, s_full, s_read, pp_full[2], pp_empty[2], o_full, o_empty, fin;
-    float power[kPowers + 3];   // l^m
-    float out_power[kC];        // scale l^{i+1}
+    uint64_t full[L::stages], empty[L::stages], vp_full[2], u_full[2], u_read[2];
+    uint64_t p_full, p_empty, s_full, s_read, pp_full[2], pp_empty[2], o_full, o_empty, fin;
+    float power[2 * kC + 4], out_power[2 * kC + 4];  // l^m and scale l^m at kC + m, m <= kC; zeros before them
     int bad[128];  // per channel of v: the segment's first token that is not finite
     uint32_t tmem;
     int abort;
   };
-  static_assert(sizeof(Misc) <= 1536 && L::bytes <= 227 * 1024, "shared memory");
+  static_assert(sizeof(Misc) <= 2048 && L::bytes <= 227 * 1024, "shared memory");
   Misc* ms = reinterpret_cast<Misc*>(smem + L::misc);
   volatile int* abort = &ms->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -145,13 +187,14 @@ __global__ void __launch_bounds__(kOut ? 640 : 384, 1)
       mbar_init(&ms->empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ms->p_full[i], 1);
-      mbar_init(&ms->p_empty[i], 4);
-      mbar_init(&ms->vp_full[i], 8);
+      mbar_init(&ms->vp_full[i], 4);
+      mbar_init(&ms->u_full[i], 1);
+      mbar_init(&ms->u_read[i], 8);
       mbar_init(&ms->pp_full[i], 4);
       mbar_init(&ms->pp_empty[i], 4);
     }
-    mbar_init(&ms->u_full, 1);
+    mbar_init(&ms->p_full, 1);
+    mbar_init(&ms->p_empty, 4);
     mbar_init(&ms->s_full, 8);
     mbar_init(&ms->s_read, 1);
     mbar_init(&ms->o_full, 1);
@@ -164,8 +207,9 @@ __global__ void __launch_bounds__(kOut ? 640 : 384, 1)
   if (threadIdx.x >= 128 && threadIdx.x < 128 + kPowers) {
     const int m = threadIdx.x - 128;
     const float f = m ? (float)exp((double)__ldg(a.log_decay + h) * m) : 1.f;
-    ms->power[m] = f;
-    if (m) ms->out_power[m - 1] = a.scale * f;
+    ms->power[kC + m] = f;
+    ms->out_power[kC + m] = a.scale * f;
+    if (m < kC) ms->power[m] = ms->out_power[m] = 0.f;
   }
   if (warp == 1) tmem_alloc(&ms->tmem, 512);
   tc_fence_before();
@@ -175,14 +219,99 @@ __global__ void __launch_bounds__(kOut ? 640 : 384, 1)
   const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;  // the warp's TMEM lanes
   constexpr int oK = (kOut ? 1 : 0) * L::tile, oV = oK + L::tile;
   bool ok = true;
+  auto all = [](bool x) { return __all_sync(0xffffffffu, x); };
 
-  if (kOut && warp < 4) regs_fewer<kRegsIssue>();
+  // The parts of l^{n-1-j} v_j of chunk c, a channel of v a thread, into TMEM
+  // (two tokens a column), the walk's third part into shared memory.
+  auto parts = [&](int c) {
+    const int st = c % L::stages, n = min(kC, valid - c * kC);
+    ok = all(mbar_wait(&ms->full[st], (c / L::stages) & 1, abort, wd));
+    if (!ok) return;
+    // The product that reads the buffer's last contents is over.  (Every warp
+    // waits, with channels or without: none may arrive for a later chunk.)
+    ok = all(mbar_wait(&ms->u_full[c % NB], ((c / NB) & 1) ^ 1, abort, wd));
+    if (!ok) return;
+    tc_fence_after();
+    const int q = warp & 3;
+    bool touched = kOut && kParts == 3;
+    if (32 * q < D) {
+      // Row j of a tile: 128 bytes, 16-byte piece x at x ^ (j % 8).  The warp's
+      // 32 channels are four pieces of block q / 2.
+      uint8_t* vt = smem + st * L::stage + oV + (q / 2) * kBlk;
+      const int p0 = 4 * (q & 1);
+      if (n < kC) {  // rows behind the sequence's end hold anything: zeros in every product
+        touched = true;
+        for (int j = n + (lane >> 2); j < kC; j += 8) {
+          const int off = j * 128 + (((p0 + (lane & 3)) ^ (j & 7)) << 4);
+          *reinterpret_cast<uint4*>(vt + off) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(vt + (oK - oV) + off) = make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+      }
+      // Fragments: the lane holds channels lane / 4 and + 8 of 16, tokens
+      // 2 (lane % 4) and the next of every 8.
+      const float* pw = ms->power + kC + n - 1 - 2 * (lane & 3);
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t v[16], part[kParts][16];
+        const int piece = p0 + 2 * hf + ((lane >> 3) & 1);
+        const uint32_t row = (lane & 7) * 128 + ((piece ^ (lane & 7)) << 4) + (lane >> 4) * 1024;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          ldsm_t(smem_u32(vt) + row + 2048 * k, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) top = __vmaxu2(top, v[k] & 0x7fff7fffu);
+        if (max(top & 0xffffu, top >> 16) >= 0x7f80u) {
+          // Not finite: 0 * NaN would reach earlier tokens of the chunk.  The
+          // value leaves the products, and its channel is NaN from here on.
+          touched = true;
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (((v[k] >> (16 * e)) & 0x7f80u) == 0x7f80u) {
+                const int j = 8 * (k >> 1) + 2 * (lane & 3) + e, x = 16 * hf + 8 * (k & 1) + (lane >> 2);
+                v[k] &= e ? 0x0000ffffu : 0xffff0000u;
+                *reinterpret_cast<uint16_t*>(vt + j * 128 + (((p0 + x / 8) ^ (j & 7)) << 4) + 2 * (x & 7)) = 0;
+                atomicMin(&ms->bad[32 * q + x], c * kC + j);
+              }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {  // behind the end the power is 0
+          float f = __fmul_rn(bf16_lo(v[k]), pw[-8 * (k >> 1)]), g = __fmul_rn(bf16_hi(v[k]), pw[-8 * (k >> 1) - 1]);
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) part[p][k] = take_part(f, g);
+        }
+        const uint32_t to = tmem + quad + ((uint32_t)(16 * hf) << 16) + vp_col<kOut>(c);
+        tmem_st_16x128b(to, part[0]);
+        tmem_st_16x128b(to + 32, part[1]);
+        if constexpr (kParts == 3) {
+          if constexpr (kOut) {
+            const uint32_t third = smem_u32(smem + L::third + (q / 2) * kBlk) + row;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              stsm_t(third + 2048 * k, part[2][4 * k], part[2][4 * k + 1], part[2][4 * k + 2], part[2][4 * k + 3]);
+          } else {
+            tmem_st_16x128b(to + 64, part[2]);
+          }
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+    }
+    if (touched) fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ms->vp_full[c % NB]);
+  };
+
+  if (warp < 4) regs_fewer<kRegsIssue>();
   if (warp == 0) {
     // ------------------------------- copies -------------------------------
     int c = 0;
     for (; c < nc; ++c) {
       const int st = c % L::stages;
-      ok = __all_sync(0xffffffffu, mbar_wait(&ms->empty[st], ((c / L::stages) & 1) ^ 1, abort, wd));
+      ok = all(mbar_wait(&ms->empty[st], ((c / L::stages) & 1) ^ 1, abort, wd));
       if (!ok) break;
       if (elect_one()) {
         uint8_t* dst = smem + st * L::stage;
@@ -209,49 +338,52 @@ __global__ void __launch_bounds__(kOut ? 640 : 384, 1)
     // -------------------------------- MMAs --------------------------------
     const uint64_t kd = smem_desc_sw128(smem), mnd = desc_mn(smem, D == 128 ? kBlk : 0);
     constexpr uint32_t idP = idesc_ab(64, 64, 0, 0), idOI = idesc_ab(128, 64, 1, 0), idOS = idesc_ab(128, 64, 0, 0),
-                       idU = idesc_ab(128, D, 1, 1);
+                       idU = idesc_ab(128, D, 0, 1), idU3 = idesc_ab(128, D, 1, 1);
     // What is ready goes first: the next scores, the next chunk's own state,
     // S^T q and V^T P' of the next chunk, each when its operands are there and
     // its accumulator has been read (a fixed order waits for one of them with
-    // the others ready: 5350 cycles a chunk).
-    auto done = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)); };
+    // the others ready).
+    auto done = [&](uint64_t* bar, int phase) { return all(mbar_test(bar, phase & 1)); };
     int ns = 0, nu = 0, nq = 0, no = 0;  // next chunk of each
     long idle = 0;
     while ((kOut ? no : nu) < nc) {
       bool some = false;
-      if (kOut && ns < nc && done(&ms->full[ns % L::stages], ns / L::stages) && done(&ms->p_empty[ns & 1], (ns >> 1) + 1)) {
+      if (nu < nc && done(&ms->vp_full[nu % NB], nu / NB) && done(&ms->u_read[nu % NB], nu / NB + 1) &&
+          done(&ms->full[nu % L::stages], nu / L::stages)) {
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (ns % L::stages) * L::stage + (kk / 4) * kBlk + (kk % 4) * 32;
-            mma_bf16(tmem + kTP + 64 * (ns & 1), desc_at(kd, off), desc_at(kd, off + oK), idP, kk > 0);
-          }
-          mma_commit(&ms->p_full[ns & 1]);
-        }
-        __syncwarp();
-        ++ns;
-        some = true;
-      }
-      if (nu < nc && done(&ms->full[nu % L::stages], nu / L::stages) && done(&ms->vp_full[nu & 1], nu >> 1) &&
-          done(&ms->s_full, kOut ? nu : nu + 1)) {
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t k0 = (nu % L::stages) * L::stage + oK, v0 = L::vpart + (nu & 1) * 3 * L::tile;
+          const uint32_t k0 = (nu % L::stages) * L::stage + oK, tu = tmem + u_col<kOut>(nu), tv = tmem + vp_col<kOut>(nu);
 #pragma unroll
           for (int p = 0; p < kParts; ++p)
 #pragma unroll
-            for (int kk = 0; kk < kC / 16; ++kk)
-              mma_bf16(tmem + kTU, desc_at(mnd, v0 + p * L::tile + kk * 2048), desc_at(mnd, k0 + kk * 2048), idU,
-                       p > 0 || kk > 0);
+            for (int kk = 0; kk < kC / 16; ++kk) {
+              if (kOut && p == 2)
+                mma_bf16(tu, desc_at(mnd, L::third + kk * 2048), desc_at(mnd, k0 + kk * 2048), idU3, 1);
+              else
+                mma_bf16_ta(tu, tv + 32 * p + 8 * kk, desc_at(mnd, k0 + kk * 2048), idU, p > 0 || kk > 0);
+            }
           if (!kOut) mma_commit(&ms->empty[nu % L::stages]);
-          mma_commit(&ms->u_full);
+          mma_commit(&ms->u_full[nu % NB]);
         }
         __syncwarp();
         ++nu;
         some = true;
       }
-      if (kOut && nq < nu && done(&ms->o_empty, nq + 1)) {
+      if (kOut && ns < nc && done(&ms->full[ns % L::stages], ns / L::stages) && done(&ms->p_empty, ns + 1)) {
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (ns % L::stages) * L::stage + (kk / 4) * kBlk + (kk % 4) * 32;
+            mma_bf16(tmem + kTP, desc_at(kd, off), desc_at(kd, off + oK), idP, kk > 0);
+          }
+          mma_commit(&ms->p_full);
+        }
+        __syncwarp();
+        ++ns;
+        some = true;
+      }
+      if (kOut && nq < ns && done(&ms->s_full, nq) && done(&ms->o_empty, nq + 1)) {  // nq < ns: q is there
         tc_fence_after();
         if (elect_one()) {
           const uint32_t q0 = (nq % L::stages) * L::stage;
@@ -267,7 +399,7 @@ __global__ void __launch_bounds__(kOut ? 640 : 384, 1)
         ++nq;
         some = true;
       }
-      if (kOut && no < nq && done(&ms->pp_full[no & 1], no >> 1)) {
+      if (kOut && no < nq && no < nu && done(&ms->pp_full[no & 1], no >> 1)) {
         tc_fence_after();
         if (elect_one()) {
           const uint32_t v0 = (no % L::stages) * L::stage + oV, p0 = L::pbuf + (no & 1) * 2 * kBlk;
@@ -297,8 +429,8 @@ __global__ void __launch_bounds__(kOut ? 640 : 384, 1)
     if (elect_one()) mma_commit(&ms->fin);
     __syncwarp();
   } else if (warp >= 4 && warp < 12) {
-    // ------------------------- the state, parts of v ----------------------
-    if (kOut) regs_more<kRegsState>();
+    // ------------------------------ the state -----------------------------
+    regs_more<kRegsState>();
     constexpr int KD = D / 2;               // channels of k of the thread's
     const int ch = 32 * (warp & 3) + lane;  // channel of v
     const int kb = (warp >> 3) * KD;        // first channel of k
@@ -327,112 +459,33 @@ __global__ void __launch_bounds__(kOut ? 640 : 384, 1)
       }
       tmem_st_wait();
       tc_fence_before();
-    };
-    // The parts of l^{n-1-j} v_j of chunk c.
-    auto parts = [&](int c) {
-      const int st = c % L::stages, n = min(kC, valid - c * kC);
-      ok = __all_sync(0xffffffffu, mbar_wait(&ms->full[st], (c / L::stages) & 1, abort, wd));
-      if (!ok) return;
-      uint8_t* kt = smem + st * L::stage + oK;
-      uint8_t* vt = smem + st * L::stage + oV;
-      uint8_t* vp = smem + L::vpart + (c & 1) * 3 * L::tile;
-      constexpr int kRows = kC * (D / 64) / 32;  // rows (of 64 channels) a thread
-      const int u = lane & 7, r0 = (warp - 4) * 4 + (lane >> 3);
-      uint4 v[kRows];
-      uint32_t m2 = 0;
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {  // row j of channel block r / 64
-        const int r = r0 + 32 * i, j = r % kC;
-        v[i] = *reinterpret_cast<const uint4*>(vt + r * 128 + ((u ^ (j & 7)) << 4));
-      }
-      if (n < kC) {  // rows behind the sequence's end hold anything: zeros in every product
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int r = r0 + 32 * i, j = r % kC;
-          if (j >= n) {
-            v[i] = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(vt + r * 128 + ((u ^ (j & 7)) << 4)) = v[i];
-            *reinterpret_cast<uint4*>(kt + r * 128 + ((u ^ (j & 7)) << 4)) = v[i];
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const uint32_t k7 = 0x7fff7fffu;
-        m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v[i].x & k7, v[i].y & k7), __vmaxu2(v[i].z & k7, v[i].w & k7)));
-      }
-      if (max(m2 & 0xffffu, m2 >> 16) >= 0x7f80u) {
-        // Not finite: 0 * NaN would reach earlier tokens of the chunk.  The
-        // value leaves the products, and its channel is NaN from here on.
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int r = r0 + 32 * i, j = r % kC;
-          uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (((w[e / 2] >> (16 * (e & 1))) & 0x7f80u) == 0x7f80u) {
-              w[e / 2] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
-              atomicMin(&ms->bad[r / kC * 64 + 8 * u + e], c * kC + j);
-            }
-          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(vt + r * 128 + ((u ^ (j & 7)) << 4)) = v[i];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int r = r0 + 32 * i, j = r % kC;
-        const float f = ms->power[max(n - 1 - j, 0)];
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t o[kParts][4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = __fmul_rn(bf16_lo(w[e]), f), y = __fmul_rn(bf16_hi(w[e]), f);
-#pragma unroll
-          for (int p = 0; p < kParts; ++p) o[p][e] = take_part(x, y);
-        }
-#pragma unroll
-        for (int p = 0; p < kParts; ++p)
-          *reinterpret_cast<uint4*>(vp + p * L::tile + r * 128 + ((u ^ (j & 7)) << 4)) =
-              make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->vp_full[c & 1]);
-    };
-    if (kOut && nc) {
-      put_state();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms->s_full);
-    }
-    if (nc) parts(0);
-    for (int c = 0; ok && c < nc; ++c) {
-      // The next chunk's parts come first where its copies are there already.
-      const int nx = (c + 1) % L::stages;
-      const bool early = c + 1 < nc && __all_sync(0xffffffffu, mbar_test(&ms->full[nx], ((c + 1) / L::stages) & 1));
-      if (early) parts(c + 1);
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&ms->u_full, c & 1, abort, wd));
+    };
+    if (kOut && nc) put_state();
+    for (int c = 0; c < nc; ++c) {
+      ok = all(mbar_wait(&ms->u_full[c % NB], (c / NB) & 1, abort, wd));
       if (!ok) break;
       tc_fence_after();
-      const float f = ms->power[min(kC, valid - c * kC)];
+      const float f = ms->power[kC + min(kC, valid - c * kC)];
 #pragma unroll
       for (int k0 = 0; k0 < KD; k0 += 32) {
         uint32_t u[32];
-        SAGESLA_TMEM_LD32(tmem + quad + kTU + kb + k0, u);
+        SAGESLA_TMEM_LD32(tmem + quad + u_col<kOut>(c) + kb + k0, u);
         tmem_ld_wait();
+        if (k0 + 32 == KD) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms->u_read[c % NB]);
+        }
 #pragma unroll
         for (int k = 0; k < 32; ++k) S[k0 + k] = __fmaf_rn(S[k0 + k], f, __uint_as_float(u[k]));
       }
-      tc_fence_before();
-      if (c + 1 < nc) {
-        if (kOut) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&ms->s_read, c & 1, abort, wd));  // S^T q has read the old state
-          if (!ok) break;
-          tc_fence_after();
-          put_state();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->s_full);
-        if (!early) parts(c + 1);
+      if (kOut && c + 1 < nc) {
+        ok = all(mbar_wait(&ms->s_read, c & 1, abort, wd));  // S^T q has read the old state
+        if (!ok) break;
+        tc_fence_after();
+        put_state();
       }
     }
     float* to = kOut ? (a.nseg > 1 || !a.state_out ? nullptr : a.state_out + bh * D * D)
@@ -442,25 +495,28 @@ __global__ void __launch_bounds__(kOut ? 640 : 384, 1)
 #pragma unroll
       for (int k = 0; k < KD; ++k) to[(size_t)(kb + k) * D + ch] = nan ? __int_as_float(0x7fffffff) : S[k];
     }
-  } else if (kOut && warp >= 12 && warp < 16) {
-    // --------------------------------- P' ---------------------------------
-    regs_fewer<kRegsP>();
+  } else if (!kOut && warp >= 12) {
+    // ------------------- parts of v of every second chunk -----------------
+    regs_more<kRegsParts>();
+    for (int c = (warp - 12) / 4; ok && c < nc; c += 2) parts(c);
+  } else if (warp >= 12 && warp < 16) {
+    // --------------------------- parts of v, P' ---------------------------
+    regs_more<kRegsOperands>();
     const int q = warp & 3, i = 16 * q + (lane & 15), jb = 32 * (lane >> 4);  // the thread's row and columns of P
-    float fac[32];  // scale l^{i-j}: the same in every chunk
-#pragma unroll
-    for (int j = 0; j < 32; ++j) fac[j] = a.scale * ms->power[max(i - jb - j, 0)];
+    const float* pw = ms->out_power + kC + i - jb;  // scale l^{i-j} at -j (zeros behind the diagonal)
     for (int c = 0; c < nc; ++c) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&ms->p_full[c & 1], (c >> 1) & 1, abort, wd));
+      parts(c);
+      if (ok) ok = all(mbar_wait(&ms->p_full, c & 1, abort, wd));
       if (!ok) break;
       tc_fence_after();
       uint32_t p[32];
-      SAGESLA_TMEM_LD2H_X32(tmem + quad + kTP + 64 * (c & 1), 32, p);
+      SAGESLA_TMEM_LD2H_X32(tmem + quad + kTP, 32, p);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->p_empty[c & 1]);
+      if (lane == 0) mbar_arrive(&ms->p_empty);
       // the outputs of two chunks ago have left this buffer
-      ok = __all_sync(0xffffffffu, mbar_wait(&ms->pp_empty[c & 1], ((c >> 1) & 1) ^ 1, abort, wd));
+      ok = all(mbar_wait(&ms->pp_empty[c & 1], ((c >> 1) & 1) ^ 1, abort, wd));
       if (!ok) break;
       uint8_t* pb = smem + L::pbuf + (c & 1) * 2 * kBlk + i * 128;
 #pragma unroll
@@ -468,8 +524,8 @@ __global__ void __launch_bounds__(kOut ? 640 : 384, 1)
         uint32_t o[2][4];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {  // a later token's score is dropped, not multiplied: it may be anything
-          float x = i - jb >= j + e ? __uint_as_float(p[j + e]) * fac[j + e] : 0.f;
-          float y = i - jb >= j + e + 1 ? __uint_as_float(p[j + e + 1]) * fac[j + e + 1] : 0.f;
+          float x = i - jb >= j + e ? __uint_as_float(p[j + e]) * pw[-(j + e)] : 0.f;
+          float y = i - jb >= j + e + 1 ? __uint_as_float(p[j + e + 1]) * pw[-(j + e + 1)] : 0.f;
           o[0][e / 2] = take_part(x, y);
           o[1][e / 2] = take_part(x, y);
         }
@@ -481,54 +537,65 @@ __global__ void __launch_bounds__(kOut ? 640 : 384, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms->pp_full[c & 1]);
     }
-  } else if (kOut && warp >= 16) {
+  } else if (warp >= 16) {
     // ------------------------------- outputs ------------------------------
-    regs_more<kRegsO>();
-    const int q = warp & 3, ch = 32 * q + lane;
+    regs_more<kRegsOut>();
+    const int q = warp & 3;
     uint16_t* out = a.o + b * a.os[0] + h * a.os[2] + (long)t0 * a.os[1];
     for (int c = 0; c < nc; ++c) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&ms->o_full, c & 1, abort, wd));
+      ok = all(mbar_wait(&ms->o_full, c & 1, abort, wd));
       if (!ok) break;
       tc_fence_after();
       const int n = min(kC, valid - c * kC);
       if (32 * q < D) {
-        // [channel of v][token] from TMEM to rows of 32 channels: 64-byte rows
-        // in shared memory, then 16 bytes a lane.  They lie where this chunk's
+        // [channel of v][token] from TMEM to rows of 32 channels: transposed by
+        // matrix stores into 64-byte rows of shared memory (piece x of row i at
+        // x ^ (i / 2 % 4)), then 16 bytes a lane.  They lie where this chunk's
         // P' was, which no MMA reads any more.
         uint8_t* ob = smem + L::pbuf + (c & 1) * 2 * kBlk + q * 4096;
-        const int bad = *reinterpret_cast<volatile int*>(&ms->bad[ch]) - c * kC;
+        const float* pw = ms->out_power + kC + 1 + 2 * (lane & 3);  // scale l^{i+1}
 #pragma unroll
-        for (int i0 = 0; i0 < kC; i0 += 32) {
-          uint32_t oi[32], os[32];
-          SAGESLA_TMEM_LD32(tmem + quad + kTOI + i0, oi);
-          SAGESLA_TMEM_LD32(tmem + quad + kTOS + i0, os);
-          tmem_ld_wait();
-          if (i0 + 32 == kC) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ms->o_empty);
-          }
-          uint16_t* to = reinterpret_cast<uint16_t*>(ob + i0 * 64) + lane;
-          if (bad < kC) {
+        for (int hf = 0; hf < 2; ++hf) {
+          const int b0 = ms->bad[32 * q + 16 * hf + (lane >> 2)] - c * kC, b1 = ms->bad[32 * q + 16 * hf + 8 + (lane >> 2)] - c * kC;
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (i0 + x >= bad) oi[x] = 0x7fffffffu;
-          }
+          for (int i0 = 0; i0 < kC; i0 += 32) {
+            const uint32_t from = tmem + quad + ((uint32_t)(16 * hf) << 16) + i0;
+            uint32_t oi[16], os[16], w[8];
+            tmem_ld_16x256b(from + kTOI, oi);
+            tmem_ld_16x256b(from + kTOS, os);
+            tmem_ld_wait();
+            if (hf == 1 && i0 + 32 == kC) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ms->o_empty);
+            }
+            if (min(b0, b1) < kC) {  // a v that was not finite: its channel is NaN from its token on
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            const __nv_bfloat162 r = __floats2bfloat162_rn(
-                __fmaf_rn(__uint_as_float(os[x]), ms->out_power[i0 + x], __uint_as_float(oi[x])),
-                __fmaf_rn(__uint_as_float(os[x + 1]), ms->out_power[i0 + x + 1], __uint_as_float(oi[x + 1])));
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(&r);
-            to[x * 32] = (uint16_t)w;
-            to[(x + 1) * 32] = (uint16_t)(w >> 16);
+              for (int x = 0; x < 16; ++x)
+                if (i0 + 8 * (x >> 2) + 2 * (lane & 3) + (x & 1) >= (x & 2 ? b1 : b0)) oi[x] = 0x7fffffffu;
+            }
+#pragma unroll
+            for (int x = 0; x < 16; x += 2) {
+              const float2 f = *reinterpret_cast<const float2*>(pw - 1 + i0 + 8 * (x >> 2));
+              const float g = pw[i0 + 8 * (x >> 2) + 1];
+              const __nv_bfloat162 r = __floats2bfloat162_rn(__fmaf_rn(__uint_as_float(os[x]), f.y, __uint_as_float(oi[x])),
+                                                             __fmaf_rn(__uint_as_float(os[x + 1]), g, __uint_as_float(oi[x + 1])));
+              w[x / 2] = *reinterpret_cast<const uint32_t*>(&r);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int i = i0 + 16 * k + 8 * (lane >> 4) + (lane & 7);
+              stsm_t(smem_u32(ob) + i * 64 + (((2 * hf + ((lane >> 3) & 1)) ^ ((i >> 1) & 3)) << 4), w[4 * k], w[4 * k + 1],
+                     w[4 * k + 2], w[4 * k + 3]);
+            }
           }
         }
         __syncwarp();
         uint16_t* row = out + (long)(c * kC + (lane >> 2)) * a.os[1] + 32 * q + 8 * (lane & 3);
 #pragma unroll
         for (int i0 = 0; i0 < kC; i0 += 8) {
-          const uint4 w = *reinterpret_cast<const uint4*>(ob + (i0 + (lane >> 2)) * 64 + 16 * (lane & 3));
+          const int i = i0 + (lane >> 2);
+          const uint4 w = *reinterpret_cast<const uint4*>(ob + i * 64 + (((lane & 3) ^ ((i >> 1) & 3)) << 4));
           if (i0 + (lane >> 2) < n) *reinterpret_cast<uint4*>(row) = w;
           row += 8 * a.os[1];
         }
@@ -649,25 +716,22 @@ cudaError_t decay_launch(DecayArgs a, int* wd, cudaStream_t st) {
       !rows_map(&mv, a.v, a.vs, a.B, a.N, a.Hk, D, a.step[2]))
     return cudaErrorInvalidValue;
   const dim3 grid(a.nseg, a.H, a.B);
-  const auto run = [&](auto* fn, int threads, int bytes) {
+  const auto run = [&](auto* fn, int bytes) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    if (threads == 640) {  // the walk's warpgroups share out exactly these registers: with fewer they would wait for ever
-      cudaFuncAttributes at;
-      if ((e = cudaFuncGetAttributes(&at, fn)) != cudaSuccess) return e;
-      if (at.numRegs < kRegs) return cudaErrorInvalidKernelImage;
-    }
-    fn<<<grid, threads, bytes, st>>>(mq, mk, mv, a, wd);
+    // The warpgroups share out exactly these registers: with fewer they would wait for ever.
+    cudaFuncAttributes at;
+    if ((e = cudaFuncGetAttributes(&at, fn)) != cudaSuccess) return e;
+    if (at.numRegs < kRegs) return cudaErrorInvalidKernelImage;
+    fn<<<grid, kThreads, bytes, st>>>(mq, mk, mv, a, wd);
     return cudaGetLastError();
   };
-  using States = Lay<D, false>;
-  using Walk = Lay<D, true>;
-  if (a.nseg == 1) return run(linear_decay_kernel<D, true, 3>, Walk::threads, Walk::bytes);
-  cudaError_t e = run(linear_decay_kernel<D, false, 3>, States::threads, States::bytes);
+  if (a.nseg == 1) return run(linear_decay_kernel<D, true, 3>, Lay<D, true>::bytes);
+  cudaError_t e = run(linear_decay_kernel<D, false, 3>, Lay<D, false>::bytes);
   if (e != cudaSuccess) return e;
   linear_decay_carry_kernel<<<dim3(D * D / 256, a.H, a.B), 256, 0, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return run(linear_decay_kernel<D, true, 2>, Walk::threads, Walk::bytes);
+  return run(linear_decay_kernel<D, true, 2>, Lay<D, true>::bytes);
 }
 
 }  // namespace

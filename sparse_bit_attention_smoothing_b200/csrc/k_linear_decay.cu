@@ -55,15 +55,13 @@ struct Lay {
   static constexpr int third = stages * stage;               // walk: the third part of v [tokens][channels]
   static constexpr int pbuf = third + (kOut ? tile : 0);     // two of P' in two parts
   static constexpr int misc = pbuf + (kOut ? 4 * kBlk : 0);
-  static constexpr int bytes = misc + 2048 + 1024;
+  static constexpr int bytes = misc + 2560 + 1024;
 };
-constexpr int kThreads = 640;
-// Registers of the five warpgroups (copies and MMAs; state, state; and in the
-// walk operands, outputs, otherwise operands twice): they share what the CTA
-// was launched with, 96 a thread.
-constexpr int kRegs = 96, kRegsIssue = 48, kRegsState = 112, kRegsOperands = 104, kRegsOut = 104, kRegsParts = 104;
-static_assert(kRegsIssue + 2 * kRegsState + kRegsOperands + kRegsOut <= 5 * kRegs, "registers");
-static_assert(kRegsIssue + 2 * kRegsState + 2 * kRegsParts <= 5 * kRegs, "registers");
+constexpr int kThreads = 768;
+// Registers of the six warpgroups (copies and MMAs, state, state, parts of v,
+// P', outputs): they share what the CTA was launched with, 80 a thread.
+constexpr int kRegs = 80, kRegsIssue = 40, kRegsState = 112, kRegsParts = 72, kRegsP = 72, kRegsOut = 72;
+static_assert(kRegsIssue + 2 * kRegsState + kRegsParts + kRegsP + kRegsOut <= 6 * kRegs, "registers");
 constexpr int kAhead = 4;  // chunks that are brought to L2 before their copy to shared memory is issued
 
 __device__ __forceinline__ uint64_t desc_mn(const void* p, uint32_t block_stride) {  // MN-major, 128-byte swizzle
@@ -148,8 +146,8 @@ __device__ __forceinline__ uint32_t take_part(float& a, float& b) {
 // kOut: the walk over a segment, with outputs.  Otherwise the segment's own
 // state.  One CTA a (segment, head, sequence).  Warps: 0 the copies, 1 the
 // MMAs, 4-11 the state (a channel of v and half of the channels of k a
-// thread), 12-15 the parts of v and P' (a segment's own state: the parts of
-// every second chunk), 16-19 the outputs (the parts of the other chunks).
+// thread), 12-15 the parts of v, 16-19 P' (a segment's own state: the parts of
+// v of every second chunk), 20-23 the outputs.
 // kParts of v: three where the state leaves the kernel, two where it only
 // feeds outputs (a walk whose states come from the carried segments).
 //
@@ -167,12 +165,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   struct Misc {
     uint64_t full[L::stages], empty[L::stages], vp_full[2], u_full[2], u_read[2];
     uint64_t p_full, p_empty, s_full, s_read, pp_full[2], pp_empty[2], o_full, o_empty, fin;
-    float power[2 * kC + 4], out_power[2 * kC + 4];  // l^m and scale l^m at kC + m, m <= kC; zeros before them
+    // l^m and scale l^m (twice, 16 banks apart) at kC + m, m <= kC; zeros before them
+    float power[2 * kC + 16], out_power[2][2 * kC + 16];
     int bad[128];  // per channel of v: the segment's first token that is not finite
     uint32_t tmem;
     int abort;
   };
-  static_assert(sizeof(Misc) <= 2048 && L::bytes <= 227 * 1024, "shared memory");
+  static_assert(sizeof(Misc) <= 2560 && L::bytes <= 227 * 1024, "shared memory");
   Misc* ms = reinterpret_cast<Misc*>(smem + L::misc);
   volatile int* abort = &ms->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -208,8 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int m = threadIdx.x - 128;
     const float f = m ? (float)exp((double)__ldg(a.log_decay + h) * m) : 1.f;
     ms->power[kC + m] = f;
-    ms->out_power[kC + m] = a.scale * f;
-    if (m < kC) ms->power[m] = ms->out_power[m] = 0.f;
+    ms->out_power[0][kC + m] = ms->out_power[1][kC + m] = a.scale * f;
+    if (m < kC) ms->power[m] = ms->out_power[0][m] = ms->out_power[1][m] = 0.f;
   }
   if (warp == 1) tmem_alloc(&ms->tmem, 512);
   tc_fence_before();
@@ -229,9 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) return;
     // The product that reads the buffer's last contents is over.  (Every warp
     // waits, with channels or without: none may arrive for a later chunk.)
-    ok = all(mbar_wait(&ms->u_full[c % NB], ((c / NB) & 1) ^ 1, abort, wd));
-    if (!ok) return;
-    tc_fence_after();
+    auto free_now = [&] {
+      ok = all(mbar_wait(&ms->u_full[c % NB], ((c / NB) & 1) ^ 1, abort, wd));
+      tc_fence_after();
+    };
     const int q = warp & 3;
     bool touched = kOut && kParts == 3;
     if (32 * q < D) {
@@ -259,9 +259,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           ldsm_t(smem_u32(vt) + row + 2048 * k, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        uint32_t top = 0;
+        uint32_t tops[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < 16; ++k) top = __vmaxu2(top, v[k] & 0x7fff7fffu);
+        for (int k = 0; k < 16; ++k) tops[k & 3] = __vmaxu2(tops[k & 3], v[k] & 0x7fff7fffu);
+        const uint32_t top = __vmaxu2(__vmaxu2(tops[0], tops[1]), __vmaxu2(tops[2], tops[3]));
         if (max(top & 0xffffu, top >> 16) >= 0x7f80u) {
           // Not finite: 0 * NaN would reach earlier tokens of the chunk.  The
           // value leaves the products, and its channel is NaN from here on.
@@ -283,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int p = 0; p < kParts; ++p) part[p][k] = take_part(f, g);
         }
+        if (hf == 0) free_now();  // the first half is computed under it
         const uint32_t to = tmem + quad + ((uint32_t)(16 * hf) << 16) + vp_col<kOut>(c);
         tmem_st_16x128b(to, part[0]);
         tmem_st_16x128b(to + 32, part[1]);
@@ -299,10 +301,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_st_wait();
       tc_fence_before();
+    } else {
+      free_now();
     }
     if (touched) fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&ms->vp_full[c % NB]);
+    if (lane == 0 && ok) mbar_arrive(&ms->vp_full[c % NB]);
   };
 
   if (warp < 4) regs_fewer<kRegsIssue>();
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (elect_one()) {
           const uint32_t k0 = (nu % L::stages) * L::stage + oK, tu = tmem + u_col<kOut>(nu), tv = tmem + vp_col<kOut>(nu);
-#pragma unroll
+#pragma unroll 1
           for (int p = 0; p < kParts; ++p)
 #pragma unroll
             for (int kk = 0; kk < kC / 16; ++kk) {
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (elect_one()) {
           const uint32_t q0 = (nq % L::stages) * L::stage;
-#pragma unroll
+#pragma unroll 1
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (elect_one()) {
           const uint32_t v0 = (no % L::stages) * L::stage + oV, p0 = L::pbuf + (no & 1) * 2 * kBlk;
-#pragma unroll
+#pragma unroll 1
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int kk = 0; kk < kC / 16; ++kk)
@@ -495,51 +499,57 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < KD; ++k) to[(size_t)(kb + k) * D + ch] = nan ? __int_as_float(0x7fffffff) : S[k];
     }
-  } else if (!kOut && warp >= 12) {
-    // ------------------- parts of v of every second chunk -----------------
-    regs_more<kRegsParts>();
-    for (int c = (warp - 12) / 4; ok && c < nc; c += 2) parts(c);
-  } else if (warp >= 12 && warp < 16) {
-    // --------------------------- parts of v, P' ---------------------------
-    regs_more<kRegsOperands>();
+  } else if (warp >= 12 && warp < (kOut ? 16 : 20)) {
+    // ------------------------------ parts of v ----------------------------
+    regs_fewer<kRegsParts>();
+    for (int c = kOut ? 0 : (warp - 12) / 4; ok && c < nc; c += kOut ? 1 : 2) parts(c);
+  } else if (kOut && warp >= 16 && warp < 20) {
+    // --------------------------------- P' ---------------------------------
+    regs_fewer<kRegsP>();
     const int q = warp & 3, i = 16 * q + (lane & 15), jb = 32 * (lane >> 4);  // the thread's row and columns of P
-    const float* pw = ms->out_power + kC + i - jb;  // scale l^{i-j} at -j (zeros behind the diagonal)
+    const float* pw = ms->out_power[lane >> 4] + kC + i - jb;  // scale l^{i-j} at -j (zeros behind the diagonal)
     for (int c = 0; c < nc; ++c) {
-      parts(c);
-      if (ok) ok = all(mbar_wait(&ms->p_full, c & 1, abort, wd));
+      ok = all(mbar_wait(&ms->p_full, c & 1, abort, wd));
       if (!ok) break;
       tc_fence_after();
-      uint32_t p[32];
-      SAGESLA_TMEM_LD2H_X32(tmem + quad + kTP, 32, p);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->p_empty);
       // the outputs of two chunks ago have left this buffer
       ok = all(mbar_wait(&ms->pp_empty[c & 1], ((c >> 1) & 1) ^ 1, abort, wd));
       if (!ok) break;
       uint8_t* pb = smem + L::pbuf + (c & 1) * 2 * kBlk + i * 128;
+#pragma unroll 1
+      for (int j0 = 0; j0 < 32; j0 += 16) {
+        uint32_t p[16];
+        SAGESLA_TMEM_LD2H_X16(tmem + quad + kTP + j0, 32, p);
+        tmem_ld_wait();
+        const float* pj = pw - j0;
+        const int d = i - jb - j0;
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) {
-        uint32_t o[2][4];
+        for (int j = 0; j < 16; j += 8) {
+          uint32_t o[2][4];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {  // a later token's score is dropped, not multiplied: it may be anything
-          float x = i - jb >= j + e ? __uint_as_float(p[j + e]) * pw[-(j + e)] : 0.f;
-          float y = i - jb >= j + e + 1 ? __uint_as_float(p[j + e + 1]) * pw[-(j + e + 1)] : 0.f;
-          o[0][e / 2] = take_part(x, y);
-          o[1][e / 2] = take_part(x, y);
+          for (int e = 0; e < 8; e += 2) {  // a later token's score is dropped, not multiplied: it may be anything
+            float x = d >= j + e ? __uint_as_float(p[j + e]) * pj[-(j + e)] : 0.f;
+            float y = d >= j + e + 1 ? __uint_as_float(p[j + e + 1]) * pj[-(j + e + 1)] : 0.f;
+            o[0][e / 2] = take_part(x, y);
+            o[1][e / 2] = take_part(x, y);
+          }
+          const uint32_t off = (((jb + j0 + j) >> 3) ^ (i & 7)) << 4;
+          *reinterpret_cast<uint4*>(pb + off) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+          *reinterpret_cast<uint4*>(pb + kBlk + off) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
         }
-        const uint32_t off = (((jb + j) >> 3) ^ (i & 7)) << 4;
-        *reinterpret_cast<uint4*>(pb + off) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-        *reinterpret_cast<uint4*>(pb + kBlk + off) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->p_empty);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms->pp_full[c & 1]);
     }
-  } else if (warp >= 16) {
+  } else if (!kOut && warp >= 20) {
+    regs_fewer<kRegsOut>();
+  } else if (warp >= 20) {
     // ------------------------------- outputs ------------------------------
-    regs_more<kRegsOut>();
+    regs_fewer<kRegsOut>();
     const int q = warp & 3;
     uint16_t* out = a.o + b * a.os[0] + h * a.os[2] + (long)t0 * a.os[1];
     for (int c = 0; c < nc; ++c) {
@@ -553,11 +563,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // x ^ (i / 2 % 4)), then 16 bytes a lane.  They lie where this chunk's
         // P' was, which no MMA reads any more.
         uint8_t* ob = smem + L::pbuf + (c & 1) * 2 * kBlk + q * 4096;
-        const float* pw = ms->out_power + kC + 1 + 2 * (lane & 3);  // scale l^{i+1}
-#pragma unroll
+        const float* pw = ms->out_power[0] + kC + 1 + 2 * (lane & 3);  // scale l^{i+1}
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           const int b0 = ms->bad[32 * q + 16 * hf + (lane >> 2)] - c * kC, b1 = ms->bad[32 * q + 16 * hf + 8 + (lane >> 2)] - c * kC;
-#pragma unroll
+#pragma unroll 1
           for (int i0 = 0; i0 < kC; i0 += 32) {
             const uint32_t from = tmem + quad + ((uint32_t)(16 * hf) << 16) + i0;
             uint32_t oi[16], os[16], w[8];
@@ -736,15 +746,19 @@ cudaError_t decay_launch(DecayArgs a, int* wd, cudaStream_t st) {
 
 }  // namespace
 
-// Segments of a sequence: as many as keep the SMs busy, where the walk that
-// they shorten is worth the second pass over k and v and two more launches
-// (in chunks: a walk takes 1 a chunk, the first pass 0.6, the launches 8).
+// Segments of a sequence: as many as there are SMs for, where the walk that
+// they shorten is worth the second pass over k and v and two more launches.  In
+// chunks of a walk (2.3 us each): both passes take 1.15 a chunk, the launches
+// and the ends of the kernels 5.  Measured, us with 1 and with s segments: 12
+// heads of 32760 tokens 1202, 171 (12); 48 of 1000 (d = 64) 37, 31 (3); 2 of
+// 500 21, 15 (8); 48 of 300 18, 33 (2); 80 of 4096 164, 193 (3: two rounds of
+// CTAs, never taken).
 int linear_decay_segments(int B, int N, int H, int sms) {
   const long heads = (long)B * H, nc = (N + kC - 1) / kC;
   long best = 1;
-  double cost = (double)nc * ((heads + sms - 1) / sms);
-  for (long s = 2; s <= nc && heads * s <= 2L * sms; ++s) {
-    const double c = 1.6 * (double)((nc + s - 1) / s) * ((heads * s + sms - 1) / sms) + 8;
+  double cost = (double)nc;
+  for (long s = 2; s <= nc && heads * s <= sms; ++s) {
+    const double c = 1.15 * (double)((nc + s - 1) / s) + 5;
     if (c < cost) cost = c, best = s;
   }
   const long per = (nc + best - 1) / best;  // chunks of a segment

@@ -318,6 +318,10 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, int x, i
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
+// One box of a 2-D tensor map -> L2.
+__device__ __forceinline__ void tma_prefetch_2d(const void* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
 // Shared memory -> one box of a 2-D tensor map (clipped at the tensor's end).
 __device__ __forceinline__ void tma_store_2d(const void* map, const void* src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),

@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int t0 = seg * a.seg_tokens, t1 = min(a.N, t0 + a.seg_tokens);
   const int valid = max(0, min(len, t1) - t0), nc = (valid + kC - 1) / kC;
   const size_t bh = (size_t)b * a.H + h;
+  if (!kOut) launch_next();
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::stages; ++s) {
       mbar_init(&ms->full[s], 1);
@@ -441,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool mine = ch < D;
     float S[KD];
     if (kOut) {
+      wait_previous();  // the carried states (all else is the caller's)
       const float* s0 = a.nseg > 1 ? a.ws + (bh * a.nseg + seg) * D * D : a.state_in ? a.state_in + bh * D * D : nullptr;
 #pragma unroll
       for (int k = 0; k < KD; ++k) S[k] = s0 && mine ? s0[(size_t)(kb + k) * D + ch] : 0.f;
@@ -635,6 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256) linear_decay_carry_kernel(const DecayArgs a) {
   const int dd = a.d * a.d, at = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y, b = blockIdx.z;
   const size_t bh = (size_t)b * a.H + h;
+  launch_next();
+  wait_previous();
   const int len = a.lens ? max(0, min(a.N, __ldg(a.lens + b))) : a.N;
   const float g = __ldg(a.log_decay + h);
   float* ws = a.ws + bh * a.nseg * dd + at;
@@ -719,6 +723,18 @@ bool rows_map(CUtensorMap* m, const void* p, const long s[3], int B, int N, int 
   return tensor_map(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Shared memory, and that the warpgroups find the registers that they share
+// out: with fewer they would wait for ever.
+cudaError_t allow_walk(const void* fn, int bytes, std::atomic<unsigned long long>& done) {
+  if (!done.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes at;
+    const cudaError_t e = cudaFuncGetAttributes(&at, fn);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs < kRegs) return cudaErrorInvalidKernelImage;
+  }
+  return allow_smem(fn, bytes, done);
+}
+
 template <int D>
 cudaError_t decay_launch(DecayArgs a, int* wd, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
@@ -726,22 +742,31 @@ cudaError_t decay_launch(DecayArgs a, int* wd, cudaStream_t st) {
       !rows_map(&mv, a.v, a.vs, a.B, a.N, a.Hk, D, a.step[2]))
     return cudaErrorInvalidValue;
   const dim3 grid(a.nseg, a.H, a.B);
-  const auto run = [&](auto* fn, int bytes) {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    // The warpgroups share out exactly these registers: with fewer they would wait for ever.
-    cudaFuncAttributes at;
-    if ((e = cudaFuncGetAttributes(&at, fn)) != cudaSuccess) return e;
-    if (at.numRegs < kRegs) return cudaErrorInvalidKernelImage;
-    fn<<<grid, kThreads, bytes, st>>>(mq, mk, mv, a, wd);
-    return cudaGetLastError();
+  // The second and third launch may start under the end of the one before.
+  const auto run = [&](auto* fn, dim3 grid, int threads, int bytes, bool chained, auto... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = chained ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
   };
-  if (a.nseg == 1) return run(linear_decay_kernel<D, true, 3>, Lay<D, true>::bytes);
-  cudaError_t e = run(linear_decay_kernel<D, false, 3>, Lay<D, false>::bytes);
+  static std::atomic<unsigned long long> done[3] = {};
+  const auto walk = [&](int i, auto* fn, int bytes, bool chained) {
+    const cudaError_t e = allow_walk(reinterpret_cast<const void*>(fn), bytes, done[i]);
+    if (e != cudaSuccess) return e;
+    return run(fn, grid, kThreads, bytes, chained, mq, mk, mv, a, wd);
+  };
+  if (a.nseg == 1) return walk(0, linear_decay_kernel<D, true, 3>, Lay<D, true>::bytes, false);
+  cudaError_t e = walk(1, linear_decay_kernel<D, false, 3>, Lay<D, false>::bytes, false);
   if (e != cudaSuccess) return e;
-  linear_decay_carry_kernel<<<dim3(D * D / 256, a.H, a.B), 256, 0, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return run(linear_decay_kernel<D, true, 2>, Lay<D, true>::bytes);
+  if ((e = run(linear_decay_carry_kernel, dim3(D * D / 256, a.H, a.B), 256, 0, true, a)) != cudaSuccess) return e;
+  return walk(2, linear_decay_kernel<D, true, 2>, Lay<D, true>::bytes, true);
 }
 
 }  // namespace

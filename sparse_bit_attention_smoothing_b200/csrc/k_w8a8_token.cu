@@ -195,6 +195,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   if (warp == 0) {
     // ------------------------------ producer ------------------------------
+    // W does not come from the kernel before this one: the first tile's rows
+    // of it are brought to L2 while the quantiser ends.
+    if (first < ntiles && elect_one()) {
+      const int n0 = (int)(first % nN) * BN + (BN / 2) * rank;
+      for (int kb = 0; kb < min(nK, 64); ++kb) tma_prefetch_2d(&mw, kb * 128, n0);
+    }
+    __syncwarp();
     wait_previous();
     const uint32_t bytes = 2 * (kStageA + (BN / 2) * 128);
     int st = 0;
@@ -541,7 +548,8 @@ cudaError_t gemm_launch(const int8_t* xq, const float* sx, const int8_t* wq, con
   const long tiles = (long)((M + 255) / 256) * ((N + BN - 1) / BN);
   const long pairs = tiles < sms / 2 ? tiles : sms / 2;
   auto* fn = w8a8_token_gemm_kernel<kType>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), kGemmSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
@@ -574,7 +582,8 @@ cudaError_t few_launch(const int8_t* xq, const float* sx, const int8_t* wq, cons
     return cudaErrorInvalidValue;
   auto* fn = w8a8_token_few_kernel<kType>;
   const int smem = S * SB + 256 + 1024;  // the sums (BN * 512 bytes) fit the ring
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), 112 * 1024, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * splits));

@@ -2,10 +2,24 @@
 // public C ABI is include/sagesla.h).  All launchers are asynchronous on
 // `st` and return the cudaGetLastError() of their launch.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
 namespace sagesla {
+
+// Raises a kernel's dynamic shared memory limit once per device (`done`: a bit
+// a device; the call costs as much as a small launch's checks).
+inline cudaError_t allow_smem(const void* fn, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Geometry shared by the launchers.
 struct Geom {

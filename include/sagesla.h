@@ -352,8 +352,8 @@ int sagesla_w8a8_token_linear(const void* x, long long ldx, const int8_t* wq, co
  *            NaN (the tables are not read out of range).
  * d a multiple of 16 from 16 to 256, rot a multiple of 16 from 0 to d; eps in
  * [0, 1]; B*N < 2^31, Hq, Hk <= 65535, B*N*(Hq+Hk) < 2^32.  Pointers 16-byte
- * aligned, strides multiples of 16 bytes and not negative; the rows of an
- * output must not overlap.  |x| below 2^60 (squares are summed in fp32).
+ * aligned, strides multiples of 16 bytes, not negative, below 2^38 elements;
+ * the rows of an output must not overlap.  |x| below 2^60 (squares are summed in fp32).
  * Nothing is allocated: the call can be captured.  Codes as sagesla_attn.
  *
  * sagesla_qk_norm_rope_bwd: its backward pass.  dq_out, dk_out: gradients of
@@ -403,8 +403,8 @@ int sagesla_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void*
  *   state_out are needed (the same for an update in place); strides is a host
  *   array of 8: batch, head of q, k, v, out.
  * d 64 or 128; Hk divides H; B*H <= 65535.  Pointers 16-byte aligned, strides
- * multiples of 8 elements and not negative (between tokens not 0), the rows of
- * out apart; out overlaps no input.  N <= 2^30.  Codes as sagesla_attn.
+ * multiples of 8 elements, not negative (between tokens not 0), below 2^38; the
+ * rows of out apart; out overlaps no input.  N <= 2^30.  Codes as sagesla_attn.
  */
 int sagesla_linear_decay_workspace(int B, int N, int H, int d, long long* bytes);
 int sagesla_linear_decay(const void* q, const void* k, const void* v, const float* log_decay, const float* state_in,

@@ -235,6 +235,13 @@ Buffers carve(uint8_t* base, const Geom& g, bool linear = false, bool q_tok = fa
   return b;
 }
 
+// An exception (memory for the maps of devices and workspaces) ends at the C
+// boundary as an error code.
+#define SAGESLA_NO_THROW \
+  catch (...) {          \
+    return SAGESLA_ERR_OOM; \
+  }
+
 inline int launch_rc(cudaError_t e) { return e == cudaSuccess ? SAGESLA_OK : SAGESLA_ERR_LAUNCH; }
 
 #define SAGESLA_TRY(x)          \
@@ -376,7 +383,7 @@ int row_strides(const int64_t* s, int B, int N, int H, int elem_bytes, long out[
   const int ext[3] = {B, N, H};
   for (int i = 0; i < 3; ++i) {
     out[i] = ext[i] > 1 ? (long)s[i] : 0;
-    if (out[i] < 0 || out[i] >= (1L << 40)) return SAGESLA_ERR_INVALID;
+    if (out[i] < 0 || out[i] >= (1L << 38)) return SAGESLA_ERR_INVALID;
     if (out[i] * elem_bytes % 16 != 0) return SAGESLA_ERR_MISALIGNED;
   }
   return SAGESLA_OK;
@@ -777,7 +784,7 @@ int sagesla_w8a8_linear(const void* x, const void* wq, const float* sw, void* y,
 
 // ------------------------------------------- W8A8 linear, per token/channel
 int sagesla_w8a8_token_quant(const void* a, int dtype, int rows, int cols, long long lda, int8_t* codes, float* scales,
-                             sagesla_stream_t stream) {
+                             sagesla_stream_t stream)try {
   if (!a || !codes || !scales) return SAGESLA_ERR_INVALID;
   SAGESLA_TRY(check_token_rows(dtype, rows, cols, lda));
   if (!aligned16(a) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u)) return SAGESLA_ERR_MISALIGNED;
@@ -786,10 +793,10 @@ int sagesla_w8a8_token_quant(const void* a, int dtype, int rows, int cols, long 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(12, st);
   return launch_rc(launch_w8a8_token_quant(a, dtype, rows, cols, rows > 1 ? lda : cols, codes, scales, st));
-}
+} SAGESLA_NO_THROW
 
 int sagesla_w8a8_token_gemm(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, const void* bias,
-                            void* y, int dtype, int M, int N, int K, sagesla_stream_t stream) {
+                            void* y, int dtype, int M, int N, int K, sagesla_stream_t stream)try {
   if (!xq || !sx) return SAGESLA_ERR_INVALID;
   SAGESLA_TRY(check_token_gemm(wq, sw, bias, y, dtype, M, N, K));
   if (!aligned16(xq) || (reinterpret_cast<uintptr_t>(sx) & 3u)) return SAGESLA_ERR_MISALIGNED;
@@ -798,7 +805,7 @@ int sagesla_w8a8_token_gemm(const int8_t* xq, const float* sx, const int8_t* wq,
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(13, st);
   return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, sm_count(dev), watchdog(dev), st, false));
-}
+} SAGESLA_NO_THROW
 
 int sagesla_w8a8_token_workspace(int M, int K, long long* bytes) {
   if (!bytes || M < 1 || K < 16 || K % 16 != 0 || K > kTokenMaxK) return SAGESLA_ERR_INVALID;
@@ -808,7 +815,7 @@ int sagesla_w8a8_token_workspace(int M, int K, long long* bytes) {
 
 int sagesla_w8a8_token_linear(const void* x, long long ldx, const int8_t* wq, const float* sw, const void* bias,
                               void* y, int dtype, int M, int N, int K, void* workspace, long long workspace_bytes,
-                              sagesla_stream_t stream) {
+                              sagesla_stream_t stream)try {
   if (!x || !workspace) return SAGESLA_ERR_INVALID;
   SAGESLA_TRY(check_token_gemm(wq, sw, bias, y, dtype, M, N, K));
   SAGESLA_TRY(check_token_rows(dtype, M, K, ldx));
@@ -829,13 +836,13 @@ int sagesla_w8a8_token_linear(const void* x, long long ldx, const int8_t* wq, co
   // The product may start under the quantiser's end, unless events between
   // the two are timing them.
   return launch_rc(launch_w8a8_token_gemm(xq, sx, wq, sw, bias, y, dtype, M, N, K, sm_count(dev), watchdog(dev), st, !ps.a));
-}
+} SAGESLA_NO_THROW
 
 // ------------------------------------------------- QK norm and rotation
 int sagesla_qk_norm_rope(const void* q, const void* k, const void* gamma_q, const void* gamma_k, float eps,
                          const float* cos, const float* sin, const int32_t* pos, void* q_out, void* k_out, int dtype,
                          int B, int N, int Hq, int Hk, int d, int rot, int T, int interleaved,
-                         const int64_t* strides, sagesla_stream_t stream) {
+                         const int64_t* strides, sagesla_stream_t stream)try {
   RopeArgs a;
   if (!strides) return SAGESLA_ERR_INVALID;
   SAGESLA_TRY(rope_common(&a, gamma_q, gamma_k, eps, cos, sin, pos, dtype, B, N, Hq, Hk, d, rot, T, interleaved));
@@ -846,9 +853,9 @@ int sagesla_qk_norm_rope(const void* q, const void* k, const void* gamma_q, cons
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(14, st);
   return launch_rc(launch_qk_norm_rope(a, dtype, interleaved != 0, false, sm_count(dev), st));
-}
+} SAGESLA_NO_THROW
 
-int sagesla_qk_norm_rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, long long* bytes) {
+int sagesla_qk_norm_rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, long long* bytes)try {
   if (!bytes || B < 1 || N < 1 || Hq < 1 || Hk < 0 || d < 16 || d > 256 || (long long)B * N > INT32_MAX || Hq > 65535 ||
       Hk > 65535)
     return SAGESLA_ERR_INVALID;
@@ -856,14 +863,14 @@ int sagesla_qk_norm_rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, long
   SAGESLA_TRY(check_device(&dev));
   *bytes = (long long)rope_bwd_workspace(B, N, Hq, Hk, d, sm_count(dev));
   return SAGESLA_OK;
-}
+} SAGESLA_NO_THROW
 
 int sagesla_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
                              const void* gamma_q, const void* gamma_k, float eps, const float* cos, const float* sin,
                              const int32_t* pos, void* dq, void* dk, float* dgamma_q, float* dgamma_k, int dtype,
                              int B, int N, int Hq, int Hk, int d, int rot, int T, int interleaved,
                              const int64_t* strides, void* workspace, long long workspace_bytes,
-                             sagesla_stream_t stream) {
+                             sagesla_stream_t stream)try {
   RopeArgs a;
   if (!strides || !dq_out || !dgamma_q || !workspace || (Hk && (!dk_out || !dgamma_k))) return SAGESLA_ERR_INVALID;
   SAGESLA_TRY(rope_common(&a, gamma_q, gamma_k, eps, cos, sin, pos, dtype, B, N, Hq, Hk, d, rot, T, interleaved));
@@ -881,22 +888,22 @@ int sagesla_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void*
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(15, st);
   return launch_rc(launch_qk_norm_rope(a, dtype, interleaved != 0, true, sm_count(dev), st));
-}
+} SAGESLA_NO_THROW
 
 // ------------------------------------------- linear attention with a decay
-int sagesla_linear_decay_workspace(int B, int N, int H, int d, long long* bytes) {
+int sagesla_linear_decay_workspace(int B, int N, int H, int d, long long* bytes)try {
   if (!bytes || B < 1 || N < 1 || H < 1 || (long long)B * H > 65535 || (d != 64 && d != 128)) return SAGESLA_ERR_INVALID;
   int dev = 0;
   SAGESLA_TRY(check_device(&dev));
   const int nseg = linear_decay_segments(B, N, H, sm_count(dev));
   *bytes = nseg > 1 ? (long long)B * H * nseg * d * d * (long long)sizeof(float) : 0;
   return SAGESLA_OK;
-}
+} SAGESLA_NO_THROW
 
 int sagesla_linear_decay(const void* q, const void* k, const void* v, const float* log_decay, const float* state_in,
                          const int32_t* lens, float scale, void* out, float* state_out, int B, int N, int H, int Hk,
                          int d, const int64_t* strides, void* workspace, long long workspace_bytes,
-                         sagesla_stream_t stream) {
+                         sagesla_stream_t stream)try {
   DecayArgs a;
   if (!strides) return SAGESLA_ERR_INVALID;
   SAGESLA_TRY(decay_common(&a, q, k, v, log_decay, state_in, scale, out, state_out, B, N, H, Hk, d));
@@ -920,11 +927,11 @@ int sagesla_linear_decay(const void* q, const void* k, const void* v, const floa
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(16, st);
   return launch_rc(launch_linear_decay(a, watchdog(dev), st));
-}
+} SAGESLA_NO_THROW
 
 int sagesla_linear_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
                               const float* state_in, float scale, void* out, float* state_out, int B, int H, int Hk,
-                              int d, const int64_t* strides, sagesla_stream_t stream) {
+                              int d, const int64_t* strides, sagesla_stream_t stream)try {
   DecayArgs a;
   if (!strides || !state_in || !state_out) return SAGESLA_ERR_INVALID;
   SAGESLA_TRY(decay_common(&a, q, k, v, log_decay, state_in, scale, out, state_out, B, 1, H, Hk, d));
@@ -940,7 +947,7 @@ int sagesla_linear_decay_step(const void* q, const void* k, const void* v, const
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(17, st);
   return launch_rc(launch_linear_decay_step(a, sm_count(dev), st));
-}
+} SAGESLA_NO_THROW
 
 int sagesla_sync_status(sagesla_stream_t stream) {
   int dev = 0;

@@ -11,11 +11,17 @@
 //
 // Bound by HBM in both directions: a row is read once and written once (the
 // backward pass recomputes r from the x it has to read anyway, so the forward
-// pass saves nothing).  A lane owns 8 consecutive channels (16 bytes of a
-// 16-bit type), L = d/8 lanes (rounded up to a power of two) a row, so a row
-// sum is log2(L) shuffles and no shared memory.  A warp serves several heads
-// of ONE token: the token's cos/sin row and gamma are loaded once for them,
-// and the loads of all its rows are in flight together.
+// pass saves nothing); what the kernels cost beside the bytes is issue slots.
+// A lane owns pieces of 8 consecutive channels (16 bytes of a 16-bit type): one
+// with interleaved pairs, the two that are each other's with pairs of halves,
+// so a rotation is arithmetic of one lane in both pairings.  (With one piece
+// the halves trade theirs by shuffles: 190 us against 168 for q of 40 heads, k
+// of 8, 32760 tokens; with two the interleaved pairs' coefficients cost a third
+// of the warps: 720p 584 us against 517.)  L = d/8 or d/16 lanes (rounded up
+// to a power of two) hold a row, so a row sum is log2(L) shuffles and no
+// shared memory.  A warp serves several heads of ONE token: the token's cos/sin
+// row and gamma are loaded once for them, and the loads of all its rows are in
+// flight together.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -144,82 +150,108 @@ __device__ __forceinline__ float dot_row(const Row& a, const Row& b) {
   return add_halves(f32x2_fma(a.e[0], b.e[0], f32x2_fma(a.e[1], b.e[1], f32x2_fma(a.e[2], b.e[2], f32x2_mul(a.e[3], b.e[3])))));
 }
 
-// The lane's part of the token's rotation: y = own * c + other * s, where
-// `other` is the pair's other channel.  Interleaved: c and s have a value a
-// pair, in the order of Row's first and second channels (s of the first ones
-// negative).  Halves: a value a channel (s negative in the first half), the
-// other channel in the lane `peer` of the row's group.
-template <bool kIl>
-struct Turn {
-  Row c, s;
-  bool on;   // the lane's channels turn
-  int peer;
+// The lane's pieces of a row: P = 1 with interleaved pairs, 2 with halves.
+template <int P>
+struct Part {
+  Row r[P];
 };
-template <bool kIl>
-__device__ __forceinline__ Turn<kIl> load_turn(const float* __restrict__ ct, const float* __restrict__ stb, long p,
-                                               int rot, int sub) {
-  Turn<kIl> t;
-  const int half = rot / 2;
-  t.on = 8 * sub < rot;
-  t.peer = sub;
-  float c[8], s[8];
-  if (kIl) {
-    float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (t.on) {
-      a = __ldg(reinterpret_cast<const float4*>(ct + p * half + 4 * sub));
-      b = __ldg(reinterpret_cast<const float4*>(stb + p * half + 4 * sub));
-    }
-    const float cc[4] = {a.x, a.y, a.z, a.w}, ss[4] = {b.x, b.y, b.z, b.w};
+template <int P>
+__device__ __forceinline__ float dot_part(const Part<P>& x, const Part<P>& y) {
+  float v = dot_row(x.r[0], y.r[0]);
+  if (P == 2) v += dot_row(x.r[P - 1], y.r[P - 1]);
+  return v;
+}
+template <int P>
+__device__ __forceinline__ Part<P> mul_part(const Part<P>& x, const Part<P>& y) {
+  Part<P> z;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[2 * i] = c[2 * i + 1] = cc[i], s[2 * i] = -ss[i], s[2 * i + 1] = ss[i];
-  } else {
-    const bool second = 8 * sub >= half;
-    const int at = second ? 8 * sub - half : 8 * sub;
-    if (t.on) t.peer = second ? sub - half / 8 : sub + half / 8;
+  for (int i = 0; i < 4 * P; ++i) z.r[i / 4].e[i % 4] = f32x2_mul(x.r[i / 4].e[i % 4], y.r[i / 4].e[i % 4]);
+  return z;
+}
+template <int P>
+__device__ __forceinline__ Part<P> mul_part(const Part<P>& x, uint64_t y) {
+  Part<P> z;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t.on) {
-        a = __ldg(reinterpret_cast<const float4*>(ct + p * half + at) + i);
-        b = __ldg(reinterpret_cast<const float4*>(stb + p * half + at) + i);
-      }
-      const float sg = second ? 1.f : -1.f;
-      c[4 * i] = a.x, c[4 * i + 1] = a.y, c[4 * i + 2] = a.z, c[4 * i + 3] = a.w;
-      s[4 * i] = sg * b.x, s[4 * i + 1] = sg * b.y, s[4 * i + 2] = sg * b.z, s[4 * i + 3] = sg * b.w;
+  for (int i = 0; i < 4 * P; ++i) z.r[i / 4].e[i % 4] = f32x2_mul(x.r[i / 4].e[i % 4], y);
+  return z;
+}
+
+// Where the lane's pieces lie (in pieces of 8 channels).  Halves, r pieces
+// turned: lane s < r/2 has pieces s and s + r/2 (channels c and c + rot/2), and
+// the lanes behind share out the rest the same way.
+template <int P>
+struct Place {
+  int at[P];
+  bool mine, on;  // the lane has channels; they turn
+  __device__ __forceinline__ Place(int d, int rot, int s) {
+    const int n = d / 8, r = rot / 8;
+    on = P * s < r;
+    mine = P * s < n;
+    if (P == 1) {
+      at[0] = s;
+    } else {
+      at[0] = on ? s : r / 2 + s;
+      at[P - 1] = on ? s + r / 2 : at[0] + (n - r) / 2;
     }
   }
-  t.c = row_of<kIl>(c);
-  t.s = row_of<kIl>(s);
+};
+
+// The lane's part of the token's rotation: y = own * c + other * s, where
+// `other` is the pair's other channel: with halves the other piece's, with
+// interleaved pairs its own neighbour (s of the first channels negative).
+template <int P>
+struct Turn {
+  Part<P> c, s;
+};
+template <int P>
+__device__ __forceinline__ Turn<P> load_turn(const float* __restrict__ ct, const float* __restrict__ stb, long p, int rot,
+                                             const Place<P>& pl) {
+  Turn<P> t;
+  const float4* c = reinterpret_cast<const float4*>(ct + p * (rot / 2)) + P * pl.at[0];
+  const float4* s = reinterpret_cast<const float4*>(stb + p * (rot / 2)) + P * pl.at[0];
+  // Interleaved: piece x has values 4x .. 4x + 3.  Halves: both pieces have 8x .. 8x + 7.
+  float4 c4[P], s4[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    c4[i] = pl.on ? __ldg(c + i) : make_float4(1.f, 1.f, 1.f, 1.f);
+    s4[i] = pl.on ? __ldg(s + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  if constexpr (P == 1) {
+    Row &cr = t.c.r[0], &sr = t.s.r[0];
+    cr.e[0] = cr.e[1] = f32x2_pack(c4[0].x, c4[0].y), cr.e[2] = cr.e[3] = f32x2_pack(c4[0].z, c4[0].w);
+    sr.e[1] = f32x2_pack(s4[0].x, s4[0].y), sr.e[3] = f32x2_pack(s4[0].z, s4[0].w);
+    sr.e[0] = neg2(sr.e[1]), sr.e[2] = neg2(sr.e[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      t.c.r[0].e[2 * i] = f32x2_pack(c4[i].x, c4[i].y), t.c.r[0].e[2 * i + 1] = f32x2_pack(c4[i].z, c4[i].w);
+      t.s.r[1].e[2 * i] = f32x2_pack(s4[i].x, s4[i].y), t.s.r[1].e[2 * i + 1] = f32x2_pack(s4[i].z, s4[i].w);
+    }
+    t.c.r[1] = t.c.r[0];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t.s.r[0].e[i] = neg2(t.s.r[1].e[i]);
+  }
   return t;
 }
 // The other channels of the lane's pairs.
-template <bool kIl>
-__device__ __forceinline__ Row others(const Row& x, int peer, int L) {
-  Row r;
-  if (kIl) {
-    r.e[0] = x.e[1], r.e[1] = x.e[0], r.e[2] = x.e[3], r.e[3] = x.e[2];
+template <int P>
+__device__ __forceinline__ Part<P> others(const Part<P>& x) {
+  Part<P> y;
+  if constexpr (P == 2) {
+    y.r[0] = x.r[1], y.r[1] = x.r[0];
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.e[i] = __shfl_sync(0xffffffffu, x.e[i], peer, L);
+    y.r[0].e[0] = x.r[0].e[1], y.r[0].e[1] = x.r[0].e[0], y.r[0].e[2] = x.r[0].e[3], y.r[0].e[3] = x.r[0].e[2];
   }
-  return r;
+  return y;
 }
-// The same of pieces as stored (halves: half the shuffles of a 16-bit type's).
-template <bool kIl, typename T>
-__device__ __forceinline__ Row other_piece(const Piece<T>& p, const Row& x, int peer, int L) {
-  if constexpr (kIl) {
-    return others<true>(x, peer, L);
-  } else {
-    Piece<T> o;
+template <int P>
+__device__ __forceinline__ Part<P> turn(const Part<P>& x, const Turn<P>& t, bool on) {
+  const Part<P> o = others(x);
+  Part<P> y = mul_part(x, t.c);
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-      o.v[i].x = __shfl_sync(0xffffffffu, p.v[i].x, peer, L);
-      o.v[i].y = __shfl_sync(0xffffffffu, p.v[i].y, peer, L);
-      o.v[i].z = __shfl_sync(0xffffffffu, p.v[i].z, peer, L);
-      o.v[i].w = __shfl_sync(0xffffffffu, p.v[i].w, peer, L);
-    }
-    return widen_row<kIl>(o);
-  }
+  for (int i = 0; i < 4 * P; ++i)
+    if (on) y.r[i / 4].e[i % 4] = f32x2_fma(o.r[i / 4].e[i % 4], t.s.r[i / 4].e[i % 4], y.r[i / 4].e[i % 4]);
+  return y;
 }
 __device__ __forceinline__ float row_sum(float v, int L) {
   for (int o = L >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -283,185 +315,187 @@ struct Group {
   }
 };
 // Rows of up to U heads: their loads are all on their way before the first is used.
-template <typename T, int U>
+template <typename T, int P, int U>
 struct Rows {
-  Piece<T> v[U];
-  __device__ __forceinline__ void load(const T* p, long step, int heads) {
+  Piece<T> v[U][P];
+  __device__ __forceinline__ void load(const T* p, const Place<P>& pl, long step, int heads) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = u < heads ? load8(p + u * step) : zero8<T>();
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[u][i] = u < heads ? load8(p + 8 * pl.at[i]) : zero8<T>();
+      p += step;
+    }
+  }
+  __device__ __forceinline__ Part<P> get(int u) const {
+    Part<P> x;
+#pragma unroll
+    for (int i = 0; i < P; ++i) x.r[i] = widen_row<P == 1>(v[u][i]);
+    return x;
   }
 };
+template <typename T, int P>
+__device__ __forceinline__ void store_part(T* p, const Place<P>& pl, const Part<P>& y) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    float v[8];
+    row_to<P == 1>(y.r[i], v);
+    store8(p + 8 * pl.at[i], v);
+  }
+}
+template <typename T, int P>
+__device__ __forceinline__ Part<P> load_part(const T* p, const Place<P>& pl) {
+  Part<P> x = {};
+  if (pl.mine)
+#pragma unroll
+    for (int i = 0; i < P; ++i) x.r[i] = widen_row<P == 1>(load8(p + 8 * pl.at[i]));
+  return x;
+}
+template <typename T, int P>
+__device__ __forceinline__ void store_zeros(T* p, const Place<P>& pl, long step, int heads) {
+  const float z[8] = {};
+  for (int u = 0; u < heads; ++u, p += step)
+#pragma unroll
+    for (int i = 0; i < P; ++i) store8(p + 8 * pl.at[i], z);
+}
 
 }  // namespace
 
 // ----------------------------------------------------------------- forward --
 // A warp takes one head group of one token (warp w of the grid: token w / G,
-// group w % G; the Gq groups of q come before k's).  What it costs beside the
-// bytes is issue slots, so up to eight rows a lane share the token's rotation,
-// the index arithmetic and the reduction.  720p (q, k of 40 heads, 3.1 GB),
-// us: four rows a warp and a reduction for each 622, eight rows 579, one
-// reduction for all 517 (6.1 TB/s); persistent warps with the next token's
-// rows on their way 771 (fewer warps).
-template <typename T, bool kIl, int U>
-__global__ void __launch_bounds__(32 * kWarps, kIl ? 3 : 2) qk_norm_rope_kernel(const RopeArgs a) {
+// group w % G; the Gq groups of q come before k's); its rows share the token's
+// rotation, the index arithmetic and one transposing reduction.
+template <typename T, int P, int U>
+__global__ void __launch_bounds__(32 * kWarps, P == 1 ? 3 : 2) qk_norm_rope_kernel(const RopeArgs a) {
   const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5), token = w / (unsigned)a.G;
   if (token >= (unsigned)a.tokens) return;
   const Group gr(a, w - token * (unsigned)a.G);
+  const Place<P> pl(a.d, a.rot, gr.sub);
   const RopeTensor& t = a.t[gr.tsr];
-  const int L = a.L, sub = gr.sub, pass = a.pass[gr.tsr];
+  const int L = a.L, pass = a.pass[gr.tsr];
   const unsigned b = a.tokens == a.N ? 0 : token / (unsigned)a.N, n = token - b * (unsigned)a.N;
-  const int heads = 8 * sub < a.d ? gr.heads : 0;
+  const int heads = pl.mine ? gr.heads : 0;
   const long xstep = (32 / L) * t.xs[2], ystep = (32 / L) * t.ys[2];
-  Rows<T, U> in;
-  in.load(static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[1] + gr.h0 * t.xs[2] + 8 * sub, xstep, heads);
-  T* y0 = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[1] + gr.h0 * t.ys[2] + 8 * sub;
+  Rows<T, P, U> in;
+  in.load(static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[1] + gr.h0 * t.xs[2], pl, xstep, heads);
+  T* y0 = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[1] + gr.h0 * t.ys[2];
   const long p = a.pos ? (long)__ldg(a.pos + token) : n;
-  if (p < 0) {  // padding: zeros
-    const float z[8] = {};
-    for (int u = 0; u < heads; ++u) store8(y0 + u * ystep, z);
+  if (p < 0) {  // padding
+    store_zeros(y0, pl, ystep, heads);
     return;
   }
   const bool far = p >= a.T;  // no such row of the tables: NaN
-  Turn<kIl> tn = load_turn<kIl>(a.cos, a.sin, far ? 0 : p, a.rot, sub);
+  Turn<P> tn = load_turn(a.cos, a.sin, far ? 0 : p, a.rot, pl);
   // gamma goes into the rotation once for all of the warp's rows
-  Row gm = {};
-  if (8 * sub < a.d) gm = widen_row<kIl>(load8(static_cast<const T*>(t.gamma) + 8 * sub));
-  const Row go = others<kIl>(gm, tn.peer, L);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    tn.c.e[i] = f32x2_mul(tn.c.e[i], gm.e[i]);
-    tn.s.e[i] = f32x2_mul(tn.s.e[i], go.e[i]);
-  }
+  const Part<P> gm = load_part(static_cast<const T*>(t.gamma), pl);
+  tn.c = mul_part(tn.c, gm);
+  tn.s = mul_part(tn.s, others(gm));
   Sums<U> r;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     r.v[u] = 0.f;
     if (u < pass) {
-      const Row f = widen_row<kIl>(in.v[u]);
-      r.v[u] = dot_row(f, f);
+      const Part<P> f = in.get(u);
+      r.v[u] = dot_part(f, f);
     }
   }
-  r.reduce(L, sub);
+  r.reduce(L, gr.sub);
   r.apply([&](float ss) { return inv_rms(ss, a, far); });
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (u >= pass) break;
-    const Row f = widen_row<kIl>(in.v[u]);
-    const Row o = other_piece<kIl>(in.v[u], f, tn.peer, L);
     const uint64_t rr = both(r.take(u, L));
-    Row y;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y.e[i] = f32x2_mul(f.e[i], tn.c.e[i]);
-      if (tn.on) y.e[i] = f32x2_fma(o.e[i], tn.s.e[i], y.e[i]);
-      y.e[i] = f32x2_mul(y.e[i], rr);
-    }
-    if (u < heads) {
-      float v[8];
-      row_to<kIl>(y, v);
-      store8(y0, v);
-    }
+    const Part<P> y = mul_part(turn(in.get(u), tn, pl.on), rr);
+    if (u < heads) store_part(y0, pl, y);
     y0 += ystep;
   }
 }
 
 // ---------------------------------------------------------------- backward --
 // Persistent: warp w keeps its head group w % G and walks the tokens w / G,
-// w / G + stride, ..., so its lanes hold the running dgamma of their eight
+// w / G + stride, ..., so its lanes hold the running dgamma of their
 // channels in fp32 registers.  The sums of a CTA's warps are joined in shared
 // memory in a fixed order and written as one partial row of q and one of k;
 // dgamma_kernel adds the CTAs' rows in fp64, again in a fixed order: no
 // atomics, the same bits every time.
-template <typename T, bool kIl, int U>
+template <typename T, int P, int U>
 __global__ void __launch_bounds__(32 * kWarps, 2) qk_norm_rope_bwd_kernel(const RopeArgs a) {
   __shared__ float part[kWarps][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, L = a.L;
   const unsigned w = blockIdx.x * kWarps + warp;
   const Group grp(a, w % (unsigned)a.G);
+  const Place<P> pl(a.d, a.rot, grp.sub);
   const RopeTensor& t = a.t[grp.tsr];
-  const int sub = grp.sub, pass = a.pass[grp.tsr];
-  const bool mine = 8 * sub < a.d;
-  const int heads = mine ? grp.heads : 0;
+  const int pass = a.pass[grp.tsr], heads = pl.mine ? grp.heads : 0;
   const long R = 32 / L, xstep = R * t.xs[2], gstep = R * t.dys[2], ystep = R * t.ys[2];
-  Row gm = {}, sums = {};
-  if (mine) gm = widen_row<kIl>(load8(static_cast<const T*>(t.gamma) + 8 * sub));
+  const Part<P> gm = load_part(static_cast<const T*>(t.gamma), pl);
+  Part<P> sums = {};
   const unsigned first = w / (unsigned)a.G;
   const bool one = a.tokens == a.N;
   for (unsigned token = first; token < (unsigned)a.tokens && first < (unsigned)a.stride; token += (unsigned)a.stride) {
     const unsigned b = one ? 0 : token / (unsigned)a.N, n = token - b * (unsigned)a.N;
-    Rows<T, U> in, gr;
-    in.load(static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[1] + grp.h0 * t.xs[2] + 8 * sub, xstep, heads);
-    gr.load(static_cast<const T*>(t.dy) + b * t.dys[0] + n * t.dys[1] + grp.h0 * t.dys[2] + 8 * sub, gstep, heads);
-    T* dx = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[1] + grp.h0 * t.ys[2] + 8 * sub;
+    Rows<T, P, U> in, gr;
+    in.load(static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[1] + grp.h0 * t.xs[2], pl, xstep, heads);
+    gr.load(static_cast<const T*>(t.dy) + b * t.dys[0] + n * t.dys[1] + grp.h0 * t.dys[2], pl, gstep, heads);
+    T* dx = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[1] + grp.h0 * t.ys[2];
     const long p = a.pos ? (long)__ldg(a.pos + token) : n;
     if (p < 0) {  // padding: no gradient
-      const float z[8] = {};
-      for (int u = 0; u < heads; ++u) store8(dx + u * ystep, z);
+      store_zeros(dx, pl, ystep, heads);
       continue;
     }
     const bool far = p >= a.T;
-    Turn<kIl> tn = load_turn<kIl>(a.cos, a.sin, far ? 0 : p, a.rot, sub);
+    Turn<P> tn = load_turn(a.cos, a.sin, far ? 0 : p, a.rot, pl);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tn.s.e[i] = neg2(tn.s.e[i]);  // turned back
+    for (int i = 0; i < 4 * P; ++i) tn.s.r[i / 4].e[i % 4] = neg2(tn.s.r[i / 4].e[i % 4]);  // turned back
     // Both row sums come from x as it is: mean(u xh) = r mean(u x), and
     //   dx = r u - x r^3 mean(u x).
     Sums<U> r, m;
-    Row g[U];
+    Part<P> g[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       r.v[u] = m.v[u] = 0.f;
       g[u] = {};
       if (u < pass) {
-        const Row f = widen_row<kIl>(in.v[u]), dyr = widen_row<kIl>(gr.v[u]);
-        const Row o = other_piece<kIl>(gr.v[u], dyr, tn.peer, L);
-        Row gm_f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          g[u].e[i] = f32x2_mul(dyr.e[i], tn.c.e[i]);
-          if (tn.on) g[u].e[i] = f32x2_fma(o.e[i], tn.s.e[i], g[u].e[i]);
-          gm_f.e[i] = f32x2_mul(f.e[i], gm.e[i]);
-        }
-        r.v[u] = dot_row(f, f);
-        m.v[u] = dot_row(g[u], gm_f);
+        const Part<P> f = in.get(u);
+        g[u] = turn(gr.get(u), tn, pl.on);
+        r.v[u] = dot_part(f, f);
+        m.v[u] = dot_part(g[u], mul_part(f, gm));
       }
     }
-    r.reduce(L, sub);
-    m.reduce(L, sub);
+    r.reduce(L, grp.sub);
+    m.reduce(L, grp.sub);
     r.apply([&](float ss) { return inv_rms(ss, a, far); });
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u >= pass) break;
       const float rv = r.take(u, L);
       const uint64_t rr = both(rv), k = both(-(rv * (m.take(u, L) * a.inv_d)) * rv * rv);  // in this order: no overflow
-      const Row f = widen_row<kIl>(in.v[u]);
-      Row y;
+      const Part<P> f = in.get(u), gs = mul_part(g[u], rr);
+      Part<P> y = mul_part(gs, gm);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint64_t gr2 = f32x2_mul(g[u].e[i], rr);
-        sums.e[i] = f32x2_fma(gr2, f.e[i], sums.e[i]);  // a lane without this head has zeros
-        y.e[i] = f32x2_fma(f.e[i], k, f32x2_mul(gr2, gm.e[i]));
+      for (int i = 0; i < 4 * P; ++i) {  // (a lane without this head has zeros)
+        sums.r[i / 4].e[i % 4] = f32x2_fma(gs.r[i / 4].e[i % 4], f.r[i / 4].e[i % 4], sums.r[i / 4].e[i % 4]);
+        y.r[i / 4].e[i % 4] = f32x2_fma(f.r[i / 4].e[i % 4], k, y.r[i / 4].e[i % 4]);
       }
-      if (u < heads) {
-        float v[8];
-        row_to<kIl>(y, v);
-        store8(dx, v);
-      }
+      if (u < heads) store_part(dx, pl, y);
       dx += ystep;
     }
   }
-  float acc[8];
-  row_to<kIl>(sums, acc);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    for (int o = L; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-  if (lane < L && mine)
+  for (int j = 0; j < P; ++j) {
+    float acc[8];
+    row_to<P == 1>(sums.r[j], acc);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part[warp][8 * sub + i] = acc[i];
+    for (int i = 0; i < 8; ++i)
+      for (int o = L; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    if (lane < L && pl.mine)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part[warp][8 * pl.at[j] + i] = acc[i];
+  }
   __syncthreads();
   const int c = threadIdx.x;
   if (c < a.d) {
     float s[2] = {0.f, 0.f};
-    for (int v = 0; v < kWarps; ++v) s[(int)(((long)blockIdx.x * kWarps + v) % a.G) >= a.Gq] += part[v][c];
+    for (int v = 0; v < kWarps; ++v) s[(int)((blockIdx.x * kWarps + v) % (unsigned)a.G) >= a.Gq] += part[v][c];
     a.part[((size_t)blockIdx.x * 2) * a.d + c] = s[0];
     a.part[((size_t)blockIdx.x * 2 + 1) * a.d + c] = s[1];
   }
@@ -489,9 +523,9 @@ namespace {
 
 constexpr int kCtasPerSm = 2;
 
-template <typename T, bool kIl>
+template <typename T, int P>
 cudaError_t rope_launch(const RopeArgs& a0, bool back, int sms, cudaStream_t st) {
-  constexpr int U = sizeof(T) == 4 ? 4 : 8, UB = sizeof(T) == 4 ? 2 : 4;
+  constexpr int U = (sizeof(T) == 4 ? 4 : 8) / P, UB = (sizeof(T) == 4 ? 2 : 4) / P;
   RopeArgs a = a0;
   const int R = 32 / a.L, most = back ? UB : U;
   // Even groups of at most `most` passes; single ones where the tokens are too
@@ -508,12 +542,12 @@ cudaError_t rope_launch(const RopeArgs& a0, bool back, int sms, cudaStream_t st)
   }
   if (!back) {
     const long ctas = (a.tokens * a.G + kWarps - 1) / kWarps;
-    qk_norm_rope_kernel<T, kIl, U><<<(unsigned)ctas, 32 * kWarps, 0, st>>>(a);
+    qk_norm_rope_kernel<T, P, U><<<(unsigned)ctas, 32 * kWarps, 0, st>>>(a);
     return cudaGetLastError();
   }
   const int ctas = rope_bwd_ctas(a.tokens, a.G, sms);
   a.stride = (long)ctas * kWarps / a.G;
-  qk_norm_rope_bwd_kernel<T, kIl, UB><<<ctas, 32 * kWarps, 0, st>>>(a);
+  qk_norm_rope_bwd_kernel<T, P, UB><<<ctas, 32 * kWarps, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   dgamma_kernel<<<dim3(a.d / 8, 2), 256, 0, st>>>(a.part, ctas, a.d, a.dgq, a.dgk);
@@ -539,15 +573,13 @@ size_t rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, int sms) {
 cudaError_t launch_qk_norm_rope(const RopeArgs& a0, int dtype, bool interleaved, bool back, int sms,
                                 cudaStream_t st) {
   RopeArgs a = a0;
-  a.L = 2;
-  while (8 * a.L < a.d) a.L <<= 1;
+  a.L = 1;
+  while ((interleaved ? 8 : 16) * a.L < a.d) a.L <<= 1;
   a.inv_d = 1.f / (float)a.d;
   if (dtype == 0)
-    return interleaved ? rope_launch<__nv_bfloat16, true>(a, back, sms, st)
-                       : rope_launch<__nv_bfloat16, false>(a, back, sms, st);
-  if (dtype == 1)
-    return interleaved ? rope_launch<__half, true>(a, back, sms, st) : rope_launch<__half, false>(a, back, sms, st);
-  return interleaved ? rope_launch<float, true>(a, back, sms, st) : rope_launch<float, false>(a, back, sms, st);
+    return interleaved ? rope_launch<__nv_bfloat16, 1>(a, back, sms, st) : rope_launch<__nv_bfloat16, 2>(a, back, sms, st);
+  if (dtype == 1) return interleaved ? rope_launch<__half, 1>(a, back, sms, st) : rope_launch<__half, 2>(a, back, sms, st);
+  return interleaved ? rope_launch<float, 1>(a, back, sms, st) : rope_launch<float, 2>(a, back, sms, st);
 }
 
 }  // namespace sagesla

@@ -62,6 +62,7 @@ constexpr int kThreads = 768;
 // P', outputs): they share what the CTA was launched with, 80 a thread.
 constexpr int kRegs = 80, kRegsIssue = 40, kRegsState = 112, kRegsParts = 72, kRegsP = 72, kRegsOut = 72;
 static_assert(kRegsIssue + 2 * kRegsState + kRegsParts + kRegsP + kRegsOut <= 6 * kRegs, "registers");
+constexpr int kMaxSegments = 256;  // a thread of the carry's CTA for each
 constexpr int kAhead = 4;  // chunks that are brought to L2 before their copy to shared memory is issued
 
 __device__ __forceinline__ uint64_t desc_mn(const void* p, uint32_t block_stride) {  // MN-major, 128-byte swizzle
@@ -637,23 +638,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256) linear_decay_carry_kernel(const DecayArgs a) {
   const int dd = a.d * a.d, at = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y, b = blockIdx.z;
   const size_t bh = (size_t)b * a.H + h;
-  launch_next();
-  wait_previous();
+  // Each segment's decay, once a CTA (64-bit exponentials in every thread took
+  // as long as the sums).
+  __shared__ float decay[kMaxSegments];
   const int len = a.lens ? max(0, min(a.N, __ldg(a.lens + b))) : a.N;
-  const float g = __ldg(a.log_decay + h);
-  float* ws = a.ws + bh * a.nseg * dd + at;
+  launch_next();
+  if (threadIdx.x < a.nseg) {
+    const int n = max(0, min(len, ((int)threadIdx.x + 1) * a.seg_tokens) - (int)threadIdx.x * a.seg_tokens);
+    decay[threadIdx.x] = n ? (float)exp((double)__ldg(a.log_decay + h) * n) : 1.f;
+  }
+  __syncthreads();
   float s = a.state_in ? a.state_in[bh * dd + at] : 0.f;
+  wait_previous();
+  float* ws = a.ws + bh * a.nseg * dd + at;
   for (int i0 = 0; i0 < a.nseg; i0 += 16) {  // sixteen segments' loads in flight
     float u[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) u[i] = i0 + i < a.nseg ? ws[(size_t)(i0 + i) * dd] : 0.f;
-    const float whole = (float)exp((double)g * a.seg_tokens);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       if (i0 + i >= a.nseg) break;
       ws[(size_t)(i0 + i) * dd] = s;
-      const int n = max(0, min(len, (i0 + i + 1) * a.seg_tokens) - (i0 + i) * a.seg_tokens);
-      s = __fmaf_rn(s, n == a.seg_tokens ? whole : n ? (float)exp((double)g * n) : 1.f, u[i]);
+      s = __fmaf_rn(s, decay[i0 + i], u[i]);
     }
   }
   if (a.state_out) a.state_out[bh * dd + at] = s;
@@ -782,7 +788,7 @@ int linear_decay_segments(int B, int N, int H, int sms) {
   const long heads = (long)B * H, nc = (N + kC - 1) / kC;
   long best = 1;
   double cost = (double)nc;
-  for (long s = 2; s <= nc && heads * s <= sms; ++s) {
+  for (long s = 2; s <= nc && heads * s <= sms && s <= kMaxSegments; ++s) {
     const double c = 1.15 * (double)((nc + s - 1) / s) + 5;
     if (c < cost) cost = c, best = s;
   }

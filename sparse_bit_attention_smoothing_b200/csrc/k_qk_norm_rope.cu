@@ -427,6 +427,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qk_norm_rope_bwd_kernel(const 
   const RopeTensor& t = a.t[grp.tsr];
   const int pass = a.pass[grp.tsr], heads = pl.mine ? grp.heads : 0;
   const long R = 32 / L, xstep = R * t.xs[2], gstep = R * t.dys[2], ystep = R * t.ys[2];
+  launch_next();
   const Part<P> gm = load_part(static_cast<const T*>(t.gamma), pl);
   Part<P> sums = {};
   const unsigned first = w / (unsigned)a.G;
@@ -503,13 +504,20 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qk_norm_rope_bwd_kernel(const 
 
 // dgamma of q (block.y 0) and k (1): eight channels a CTA, its 32 threads of a
 // channel add the CTAs' partial rows in fp64.
-__global__ void __launch_bounds__(256) dgamma_kernel(const float* __restrict__ part, int rows, int d,
+__global__ void __launch_bounds__(256) dgamma_kernel(const float* part, int rows, int d,
                                                      float* __restrict__ gq, float* __restrict__ gk) {
   __shared__ double s[32][8];
   float* out = blockIdx.y ? gk : gq;
   const int c = blockIdx.x * 8 + (threadIdx.x & 7), r0 = threadIdx.x >> 3;
   double v = 0.0;
-  for (int r = r0; r < rows; r += 32) v += (double)part[((size_t)r * 2 + blockIdx.y) * d + c];
+  wait_previous();
+  for (int r = r0; r < rows; r += 32 * 10) {  // ten rows' loads in flight
+    float x[10];
+#pragma unroll
+    for (int i = 0; i < 10; ++i) x[i] = r + 32 * i < rows ? part[((size_t)(r + 32 * i) * 2 + blockIdx.y) * d + c] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) v += (double)x[i];
+  }
   s[r0][threadIdx.x & 7] = v;
   __syncthreads();
   if (threadIdx.x < 8 && out) {
@@ -548,10 +556,18 @@ cudaError_t rope_launch(const RopeArgs& a0, bool back, int sms, cudaStream_t st)
   const int ctas = rope_bwd_ctas(a.tokens, a.G, sms);
   a.stride = (long)ctas * kWarps / a.G;
   qk_norm_rope_bwd_kernel<T, P, UB><<<ctas, 32 * kWarps, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  dgamma_kernel<<<dim3(a.d / 8, 2), 256, 0, st>>>(a.part, ctas, a.d, a.dgq, a.dgk);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};  // may start under the end of the kernel before
+  cfg.gridDim = dim3(a.d / 8, 2);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dgamma_kernel, static_cast<const float*>(a.part), ctas, a.d, a.dgq, a.dgk);
 }
 
 }  // namespace

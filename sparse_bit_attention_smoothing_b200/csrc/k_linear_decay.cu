@@ -13,14 +13,27 @@
 // state (its channel of v, all channels of k) in fp32 registers, and S and P'
 // never need a transposition.  What is not bf16 by itself is held in bf16
 // parts whose sum is it: P' and S, which end in a bf16 output, in two parts
-// (2^-16), l^{n-1-j} v_j, which ends in the fp32 state, in three (2^-24:
-// with two the state is off by 3e-6, with three by 2e-7).
+// (2^-16 of the value is left), l^{n-1-j} v_j, which ends in the fp32 state, in
+// three (2^-24).
 //
-// Bound by HBM (4 rows of d a token and head, 64 KB a chunk at d = 128, 2850
-// cycles of an SM's share).  Few heads do not fill the SMs, so a long sequence
-// is cut into segments: a first launch sums each segment's own state, a second
-// one carries the states across the segments, the third walks each segment
-// from its state.  That reads k and v twice.
+// HBM would allow 65 us at 12 heads of 32760 tokens of 128 (4 rows of d a token
+// and head); 158 us measured.  Bound by latency: a chunk is 540 ns of an SM's
+// share of HBM and 1700 cycles of the tensor pipe, but 4300 cycles (2.35 us)
+// from one to the next, in which every step waits for another one: parts of v
+// (2900 cycles of a warpgroup), products, the state (1650), S^T q, outputs (1300
+// until their accumulator is free).  So each is a warpgroup of its own, with
+// two buffers between them where TMEM has the columns.  Measured on the way
+// (the same case, us): one order of the products for all chunks 224; what is
+// ready first 171; the next chunk's own state beside the state that is still
+// read (two areas), one test for all barriers, a second warp for the products
+// of the outputs 165; the copies without a prefetch to L2 four chunks ahead 158.
+// Slower: unrolled loops (184: the roles' code has to stay in the instruction
+// cache), half chunks of v (178), two warpgroups for the outputs (159).
+//
+// Few heads do not fill the SMs, so a long sequence is cut into segments: a
+// first launch sums each segment's own state, a second one carries the states
+// across the segments, the third walks each segment from its state.  That reads
+// k and v twice.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -36,21 +49,28 @@ constexpr int kBlk = kC * 128;    // 64 tokens x 64 channels of bf16: rows of 12
 constexpr int kPowers = kC + 1;
 
 // TMEM columns.  v parts: l^{n-1-j} v_j [channels of v][two tokens a column],
-// 32 columns a part.
-constexpr uint32_t kTP = 0;      // walk: P (64 rows: lanes 0-15 of each quadrant)
-constexpr uint32_t kTOI = 128;   //       sum_j v_j P'_ij  [channels of v][i]
-constexpr uint32_t kTOS = 192;   //       S^T q_i          [channels of v][i]
-constexpr uint32_t kTSH = 384, kTSL = 448;  // S^T in two bf16 parts, two channels of k a column
+// 32 columns a part.  The walk:
+//   two buffers of P (64 rows: lanes 0-15 of each quadrant), each in turn
+//   sum_j v_j P'_ij [channels of v][i] when P has been read;
+//   S^T q_i [channels of v][i];
+//   two areas of the state.  Chunk c's own state [channels of v][of k] comes
+//   into area c + 1, and the threads that read it put the state before chunk
+//   c + 1 in its place (S^T in two bf16 parts, two channels of k a column, each
+//   warpgroup's high parts and then its low ones) while the state before chunk
+//   c is still read in area c.
+constexpr uint32_t kTOS = 192;
+__device__ __forceinline__ uint32_t oi_col(int c) { return (c & 1) * 64; }
+__device__ __forceinline__ uint32_t s_col(int c) { return 256 + (c & 1) * 128; }
 template <bool kOut>
-__device__ __forceinline__ uint32_t vp_col(int c) { return kOut ? 64 : (c & 1) * 96; }
+__device__ __forceinline__ uint32_t vp_col(int c) { return kOut ? 128 : (c & 1) * 96; }
 template <bool kOut>
-__device__ __forceinline__ uint32_t u_col(int c) { return kOut ? 256 : 256 + (c & 1) * 128; }  // [channels of v][of k]
+__device__ __forceinline__ uint32_t u_col(int c) { return s_col(kOut ? c + 1 : c); }
 
 template <int D, bool kOut>
 struct Lay {
   static constexpr int tile = D / 64 * kBlk;                 // one tensor's chunk
   static constexpr int tensors = kOut ? 3 : 2;               // (q), k, v
-  static constexpr int stages = kOut ? 3 : 5;
+  static constexpr int stages = D == 64 ? (kOut ? 6 : 8) : kOut ? 3 : 5;
   static constexpr int stage = tensors * tile;
   static constexpr int third = stages * stage;               // walk: the third part of v [tokens][channels]
   static constexpr int pbuf = third + (kOut ? tile : 0);     // two of P' in two parts
@@ -63,7 +83,6 @@ constexpr int kThreads = 768;
 constexpr int kRegs = 80, kRegsIssue = 40, kRegsState = 112, kRegsParts = 72, kRegsP = 72, kRegsOut = 72;
 static_assert(kRegsIssue + 2 * kRegsState + kRegsParts + kRegsP + kRegsOut <= 6 * kRegs, "registers");
 constexpr int kMaxSegments = 256;  // a thread of the carry's CTA for each
-constexpr int kAhead = 4;  // chunks that are brought to L2 before their copy to shared memory is issued
 
 __device__ __forceinline__ uint64_t desc_mn(const void* p, uint32_t block_stride) {  // MN-major, 128-byte swizzle
   uint64_t d = (uint64_t)((smem_u32(p) >> 4) & 0x3FFF);
@@ -97,12 +116,6 @@ template <int kN>
 __device__ __forceinline__ void regs_fewer() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN));
 }
-__device__ __forceinline__ void tma_prefetch_4d(const void* map, int x, int n, int h, int b) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(x), "r"(n),
-               "r"(h), "r"(b)
-               : "memory");
-}
-
 // 16 lanes in fragments of 8 x 8 16-bit matrices.  Store: register 2k holds,
 // of lane t/4, column 4k + t%4, register 2k + 1 the same of lane t/4 + 8.
 __device__ __forceinline__ void tmem_st_16x128b(uint32_t addr, const uint32_t (&r)[16]) {
@@ -146,15 +159,15 @@ __device__ __forceinline__ uint32_t take_part(float& a, float& b) {
 
 // kOut: the walk over a segment, with outputs.  Otherwise the segment's own
 // state.  One CTA a (segment, head, sequence).  Warps: 0 the copies, 1 the
-// MMAs, 4-11 the state (a channel of v and half of the channels of k a
-// thread), 12-15 the parts of v, 16-19 P' (a segment's own state: the parts of
-// v of every second chunk), 20-23 the outputs.
+// MMAs (of a walk: those that do not need the state, 2 the others), 4-11 the
+// state (a channel of v and half of the channels of k a thread), 12-15 the
+// parts of v, 16-19 P' (a segment's own state: the parts of v of every second
+// chunk), 20-23 the outputs.
 // kParts of v: three where the state leaves the kernel, two where it only
 // feeds outputs (a walk whose states come from the carried segments).
 //
-// What the design turns on is shared memory's bandwidth: the walk's MMAs read
-// 100 KB of it a chunk with the parts of v in TMEM, 170 KB with them in shared
-// memory (and two chunks' copies fit then, not three).
+// The parts of v are in TMEM: from shared memory the walk's MMAs would read
+// 170 KB of it a chunk, not 100 KB, and two chunks' copies would fit, not three.
 template <int D, bool kOut, int kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_decay_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -165,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   struct Misc {
     uint64_t full[L::stages], empty[L::stages], vp_full[2], u_full[2], u_read[2];
-    uint64_t p_full, p_empty, s_full, s_read, pp_full[2], pp_empty[2], o_full, o_empty, fin;
+    uint64_t p_full[2], s_full[2], s_read[2], pp_full[2], pp_empty[2], o_full, o_empty[2], fin;
     // l^m and scale l^m (twice, 16 banks apart) at kC + m, m <= kC; zeros before them
     float power[2 * kC + 16], out_power[2][2 * kC + 16];
     int bad[128];  // per channel of v: the segment's first token that is not finite
@@ -185,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::stages; ++s) {
       mbar_init(&ms->full[s], 1);
-      mbar_init(&ms->empty[s], 1);
+      mbar_init(&ms->empty[s], kOut ? 2 : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms->vp_full[i], 4);
@@ -193,14 +206,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ms->u_read[i], 8);
       mbar_init(&ms->pp_full[i], 4);
       mbar_init(&ms->pp_empty[i], 4);
+      mbar_init(&ms->p_full[i], 1);
+      mbar_init(&ms->s_full[i], 8);
+      mbar_init(&ms->s_read[i], 1);
+      mbar_init(&ms->o_empty[i], 4);
     }
-    mbar_init(&ms->p_full, 1);
-    mbar_init(&ms->p_empty, 4);
-    mbar_init(&ms->s_full, 8);
-    mbar_init(&ms->s_read, 1);
     mbar_init(&ms->o_full, 1);
-    mbar_init(&ms->o_empty, 4);
-    mbar_init(&ms->fin, 1);
+    mbar_init(&ms->fin, kOut ? 2 : 1);
     ms->abort = 0;
     mbar_fence_init();
   }
@@ -231,7 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The product that reads the buffer's last contents is over.  (Every warp
     // waits, with channels or without: none may arrive for a later chunk.)
     auto free_now = [&] {
-      ok = all(mbar_wait(&ms->u_full[c % NB], ((c / NB) & 1) ^ 1, abort, wd));
+      const int u = c + 2 - NB;  // that of the chunk NB before
+      ok = all(mbar_wait(&ms->u_full[u & 1], ((u / 2) & 1) ^ 1, abort, wd));
       tc_fence_after();
     };
     const int q = warp & 3;
@@ -322,14 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) {
         uint8_t* dst = smem + st * L::stage;
         mbar_expect_tx(&ms->full[st], L::stage);
-        const int n = t0 + c * kC, ahead = n + kAhead * kC;
+        const int n = t0 + c * kC;
 #pragma unroll
         for (int x = 0; x < D; x += 64) {
-          if (c + kAhead < nc) {
-            tma_prefetch_4d(&mk, x, ahead, hk * a.step[1][0], b * a.step[1][1]);
-            if (kOut) tma_prefetch_4d(&mq, x, ahead, h * a.step[0][0], b * a.step[0][1]);
-            tma_prefetch_4d(&mv, x, ahead, hk * a.step[2][0], b * a.step[2][1]);
-          }
           tma_load_4d(dst + oK + x / 64 * kBlk, &mk, x, n, hk * a.step[1][0], b * a.step[1][1], &ms->full[st]);
           if (kOut) tma_load_4d(dst + x / 64 * kBlk, &mq, x, n, h * a.step[0][0], b * a.step[0][1], &ms->full[st]);
           tma_load_4d(dst + oV + x / 64 * kBlk, &mv, x, n, hk * a.step[2][0], b * a.step[2][1], &ms->full[st]);
@@ -340,22 +348,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The copies are over before the CTA ends, also where a role gave up.
     for (int g = max(0, c - L::stages); g < c; ++g)
       if (!mbar_wait_drain(&ms->full[g % L::stages], (g / L::stages) & 1, wd)) break;
-  } else if (warp == 1) {
+  } else if (warp == 1 || (kOut && warp == 2)) {
     // -------------------------------- MMAs --------------------------------
     const uint64_t kd = smem_desc_sw128(smem), mnd = desc_mn(smem, D == 128 ? kBlk : 0);
     constexpr uint32_t idP = idesc_ab(64, 64, 0, 0), idOI = idesc_ab(128, 64, 1, 0), idOS = idesc_ab(128, 64, 0, 0),
                        idU = idesc_ab(128, D, 0, 1), idU3 = idesc_ab(128, D, 1, 1);
-    // What is ready goes first: the next scores, the next chunk's own state,
-    // S^T q and V^T P' of the next chunk, each when its operands are there and
+    // What is ready goes first, each product when its operands are there and
     // its accumulator has been read (a fixed order waits for one of them with
-    // the others ready).
-    auto done = [&](uint64_t* bar, int phase) { return all(mbar_test(bar, phase & 1)); };
-    int ns = 0, nu = 0, nq = 0, no = 0;  // next chunk of each
+    // the others ready).  A lane watches a barrier, so that one test asks for
+    // all of them.
+    constexpr uint32_t kOS = 0x103, kU = 0x1c, kP = 0x60, kOI = 0x280;  // the lanes of each
+    uint64_t* bar = ms->s_full;  // its buffers, how many, the next one and its phase
+    int bufs = 2, buf = 0, phase = 0;
+    if (lane == 1) bar = ms->o_empty, buf = 1, phase = 1;  // of the chunk before
+    if (lane == 2) bar = ms->vp_full, bufs = NB;
+    if (lane == 3 || lane == 5 || lane == 8) bar = ms->full, bufs = L::stages;
+    // its area: the state before the last chunk was in it (a segment's own: the last but one)
+    if (lane == 4) bar = kOut ? ms->s_read : ms->u_read, buf = kOut, phase = 1;
+    if (lane == 6) bar = ms->o_empty, phase = 1;  // of the chunk two before
+    if (lane == 7) bar = ms->pp_full;
+    if (lane == 9) bar = ms->u_full;  // v has no NaN left
+    auto next = [&](uint32_t lanes) {
+      if ((lanes >> lane & 1) && ++buf == bufs) buf = 0, phase ^= 1;
+    };
+    int ns = 0, nu = 0, nq = 0, no = 0, ne = 0;  // next chunk of each; next one whose copy is read
     long idle = 0;
-    while ((kOut ? no : nu) < nc) {
+    const bool outs = warp == 2;  // S^T q and V^T P', else the chunk's own state and P
+    while ((kOut ? ne : nu) < nc) {
+      const uint32_t ready = __ballot_sync(0xffffffffu, mbar_test(bar + buf, phase));
       bool some = false;
-      if (nu < nc && done(&ms->vp_full[nu % NB], nu / NB) && done(&ms->u_read[nu % NB], nu / NB + 1) &&
-          done(&ms->full[nu % L::stages], nu / L::stages)) {
+      __syncwarp();
+      if (kOut && outs && nq < nc && (ready & kOS) == kOS) {
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t q0 = (nq % L::stages) * L::stage, ts = tmem + s_col(nq);
+#pragma unroll 1
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16_ta(tmem + kTOS, ts + (kk / (D / 32)) * (D / 2) + p * (D / 4) + kk % (D / 32) * 8,
+                          desc_at(kd, q0 + (kk / 4) * kBlk + (kk % 4) * 32), idOS, p > 0 || kk > 0);
+          mma_commit(&ms->s_read[nq & 1]);
+          if (no > nq) mma_commit(&ms->o_full);
+        }
+        __syncwarp();
+        ++nq;
+        next(kOS);
+        some = true;
+      }
+      if (!outs && nu < nc && (ready & kU) == kU) {
         tc_fence_after();
         if (elect_one()) {
           const uint32_t k0 = (nu % L::stages) * L::stage + oK, tu = tmem + u_col<kOut>(nu), tv = tmem + vp_col<kOut>(nu);
@@ -369,43 +410,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_bf16_ta(tu, tv + 32 * p + 8 * kk, desc_at(mnd, k0 + kk * 2048), idU, p > 0 || kk > 0);
             }
           if (!kOut) mma_commit(&ms->empty[nu % L::stages]);
-          mma_commit(&ms->u_full[nu % NB]);
+          mma_commit(&ms->u_full[nu & 1]);
         }
         __syncwarp();
         ++nu;
+        next(kU);
         some = true;
       }
-      if (kOut && ns < nc && done(&ms->full[ns % L::stages], ns / L::stages) && done(&ms->p_empty, ns + 1)) {
+      if (kOut && !outs && ns < nc && (ready & kP) == kP) {
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (ns % L::stages) * L::stage + (kk / 4) * kBlk + (kk % 4) * 32;
-            mma_bf16(tmem + kTP, desc_at(kd, off), desc_at(kd, off + oK), idP, kk > 0);
+            mma_bf16(tmem + oi_col(ns), desc_at(kd, off), desc_at(kd, off + oK), idP, kk > 0);
           }
-          mma_commit(&ms->p_full);
+          mma_commit(&ms->p_full[ns & 1]);
         }
         __syncwarp();
         ++ns;
+        next(kP);
         some = true;
       }
-      if (kOut && nq < ns && done(&ms->s_full, nq) && done(&ms->o_empty, nq + 1)) {  // nq < ns: q is there
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t q0 = (nq % L::stages) * L::stage;
-#pragma unroll 1
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16_ta(tmem + kTOS, tmem + (p ? kTSL : kTSH) + kk * 8, desc_at(kd, q0 + (kk / 4) * kBlk + (kk % 4) * 32),
-                          idOS, p > 0 || kk > 0);
-          mma_commit(&ms->s_read);
-        }
-        __syncwarp();
-        ++nq;
-        some = true;
-      }
-      if (kOut && no < nq && no < nu && done(&ms->pp_full[no & 1], no >> 1)) {
+      if (kOut && outs && no < nc && (ready & kOI) == kOI) {
         tc_fence_after();
         if (elect_one()) {
           const uint32_t v0 = (no % L::stages) * L::stage + oV, p0 = L::pbuf + (no & 1) * 2 * kBlk;
@@ -413,18 +440,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int kk = 0; kk < kC / 16; ++kk)
-              mma_bf16(tmem + kTOI, desc_at(mnd, v0 + kk * 2048), desc_at(kd, p0 + p * kBlk + kk * 32), idOI,
+              mma_bf16(tmem + oi_col(no), desc_at(mnd, v0 + kk * 2048), desc_at(kd, p0 + p * kBlk + kk * 32), idOI,
                        p > 0 || kk > 0);
-          mma_commit(&ms->o_full);
-          mma_commit(&ms->empty[no % L::stages]);
+          if (nq > no) mma_commit(&ms->o_full);
         }
         __syncwarp();
         ++no;
+        next(kOI);
         some = true;
       }
-      idle = some ? 0 : idle + 1;
-      ok = !__any_sync(0xffffffffu, *abort || idle > kSpinLimit);
-      if (!ok) {
+      // both of the warp's products have read it
+      if (kOut && (outs ? ne < nq && ne < no : ne < nu && ne < ns)) {
+        if (elect_one()) mma_commit(&ms->empty[ne % L::stages]);
+        __syncwarp();
+        ++ne;
+      }
+      if (some) {
+        idle = 0;
+      } else if (__any_sync(0xffffffffu, *abort || ++idle > kSpinLimit)) {
         if (lane == 0 && !*abort) {
           *abort = 1;
           atomicExch(wd, 1);
@@ -451,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < KD; ++k) S[k] = 0.f;
     }
-    auto put_state = [&]() {  // S^T in two bf16 parts, the A operand of S^T q
+    auto put_state = [&](int c) {  // S^T in two bf16 parts, the A operand of chunk c's S^T q
+      const uint32_t to = tmem + quad + s_col(c) + kb;
 #pragma unroll
       for (int k0 = 0; k0 < KD; k0 += 32) {
         uint32_t hi[16], lo[16];
@@ -461,17 +495,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           hi[k / 2] = take_part(x, y);
           lo[k / 2] = take_part(x, y);
         }
-        SAGESLA_TMEM_ST16(tmem + quad + kTSH + (kb + k0) / 2, hi);
-        SAGESLA_TMEM_ST16(tmem + quad + kTSL + (kb + k0) / 2, lo);
+        SAGESLA_TMEM_ST16(to + k0 / 2, hi);
+        SAGESLA_TMEM_ST16(to + KD / 2 + k0 / 2, lo);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->s_full);
+      if (lane == 0) mbar_arrive(&ms->s_full[c & 1]);
     };
-    if (kOut && nc) put_state();
+    if (kOut && nc) put_state(0);
     for (int c = 0; c < nc; ++c) {
-      ok = all(mbar_wait(&ms->u_full[c % NB], (c / NB) & 1, abort, wd));
+      ok = all(mbar_wait(&ms->u_full[c & 1], (c / 2) & 1, abort, wd));
       if (!ok) break;
       tc_fence_after();
       const float f = ms->power[kC + min(kC, valid - c * kC)];
@@ -480,20 +514,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t u[32];
         SAGESLA_TMEM_LD32(tmem + quad + u_col<kOut>(c) + kb + k0, u);
         tmem_ld_wait();
-        if (k0 + 32 == KD) {
+        if (!kOut && k0 + 32 == KD) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ms->u_read[c % NB]);
+          if (lane == 0) mbar_arrive(&ms->u_read[c & 1]);
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k) S[k0 + k] = __fmaf_rn(S[k0 + k], f, __uint_as_float(u[k]));
       }
-      if (kOut && c + 1 < nc) {
-        ok = all(mbar_wait(&ms->s_read, c & 1, abort, wd));  // S^T q has read the old state
-        if (!ok) break;
-        tc_fence_after();
-        put_state();
-      }
+      if (kOut && c + 1 < nc) put_state(c + 1);
     }
     float* to = kOut ? (a.nseg > 1 || !a.state_out ? nullptr : a.state_out + bh * D * D)
                      : a.ws + (bh * a.nseg + seg) * D * D;
@@ -512,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, i = 16 * q + (lane & 15), jb = 32 * (lane >> 4);  // the thread's row and columns of P
     const float* pw = ms->out_power[lane >> 4] + kC + i - jb;  // scale l^{i-j} at -j (zeros behind the diagonal)
     for (int c = 0; c < nc; ++c) {
-      ok = all(mbar_wait(&ms->p_full, c & 1, abort, wd));
+      ok = all(mbar_wait(&ms->p_full[c & 1], (c >> 1) & 1, abort, wd));
       if (!ok) break;
       tc_fence_after();
       // the outputs of two chunks ago have left this buffer
@@ -522,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int j0 = 0; j0 < 32; j0 += 16) {
         uint32_t p[16];
-        SAGESLA_TMEM_LD2H_X16(tmem + quad + kTP + j0, 32, p);
+        SAGESLA_TMEM_LD2H_X16(tmem + quad + oi_col(c) + j0, 32, p);
         tmem_ld_wait();
         const float* pj = pw - j0;
         const int d = i - jb - j0;
@@ -542,8 +571,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->p_empty);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms->pp_full[c & 1]);
@@ -574,13 +601,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i0 = 0; i0 < kC; i0 += 32) {
             const uint32_t from = tmem + quad + ((uint32_t)(16 * hf) << 16) + i0;
             uint32_t oi[16], os[16], w[8];
-            tmem_ld_16x256b(from + kTOI, oi);
+            tmem_ld_16x256b(from + oi_col(c), oi);
             tmem_ld_16x256b(from + kTOS, os);
             tmem_ld_wait();
             if (hf == 1 && i0 + 32 == kC) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&ms->o_empty);
+              if (lane == 0) mbar_arrive(&ms->o_empty[c & 1]);
             }
             if (min(b0, b1) < kC) {  // a v that was not finite: its channel is NaN from its token on
 #pragma unroll
@@ -615,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms->pp_empty[c & 1]);
       } else if (lane == 0) {
-        mbar_arrive(&ms->o_empty);
+        mbar_arrive(&ms->o_empty[c & 1]);
         mbar_arrive(&ms->pp_empty[c & 1]);
       }
     }
@@ -666,7 +693,8 @@ __global__ void __launch_bounds__(256) linear_decay_carry_kernel(const DecayArgs
 }
 
 // ----------------------------------------------------------- single tokens --
-// Bound by the state's bytes (read and written once).  A CTA holds CW columns
+// Bound by the state's bytes (read and written once): 64 sequences of 40 heads
+// take 54 us, 6.3 TB/s; one of 40 heads is all latency (4.9 us).  A CTA holds CW columns
 // of one head's state, four a thread; all of a thread's loads are in flight
 // before the first product.
 template <int D, int CW>
@@ -779,17 +807,17 @@ cudaError_t decay_launch(DecayArgs a, int* wd, cudaStream_t st) {
 
 // Segments of a sequence: as many as there are SMs for, where the walk that
 // they shorten is worth the second pass over k and v and two more launches.  In
-// chunks of a walk (2.3 us each): both passes take 1.15 a chunk, the launches
+// chunks of a walk (2.35 us each): both passes take 1.34 a chunk, the launches
 // and the ends of the kernels 5.  Measured, us with 1 and with s segments: 12
-// heads of 32760 tokens 1202, 171 (12); 48 of 1000 (d = 64) 37, 31 (3); 2 of
-// 500 21, 15 (8); 48 of 300 18, 33 (2); 80 of 4096 164, 193 (3: two rounds of
-// CTAs, never taken).
+// heads of 32760 tokens 1204, 160 (12); 8 of 4096 156, 28 (16); 48 of 1000 (d =
+// 64) 36, 31 (3); 2 of 500 20, 10 (8); 48 of 300 18, 33 (3); 80 of 4096 161, 188
+// (3: two rounds of CTAs, never taken).
 int linear_decay_segments(int B, int N, int H, int sms) {
   const long heads = (long)B * H, nc = (N + kC - 1) / kC;
   long best = 1;
   double cost = (double)nc;
   for (long s = 2; s <= nc && heads * s <= sms && s <= kMaxSegments; ++s) {
-    const double c = 1.15 * (double)((nc + s - 1) / s) + 5;
+    const double c = 1.34 * (double)((nc + s - 1) / s) + 5;
     if (c < cost) cost = c, best = s;
   }
   const long per = (nc + best - 1) / best;  // chunks of a segment

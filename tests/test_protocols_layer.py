@@ -1,5 +1,5 @@
 """The barrier protocols of the linear attention with a decay, on the CPU, with
-the scheduler and the checks of test_protocols.py.
+the scheduler and the conditions of test_protocols.py.
 
 A product that an MMA-issuing warp serves is a role of its own here (the warp
 takes whichever is ready, so the products of one warp meet in any order), and
@@ -173,26 +173,26 @@ def test_own_state_protocol(n, stages, turn):
         simulate(P, C, seed)
 
 
-def test_checker_catches_three_warpgroups_for_the_parts():
+def test_the_model_catches_three_warpgroups_for_the_parts():
     # a third warpgroup may stand two phases before the product it waits for
     P, C = own_state_programs(12, groups=3)
     assert _caught(P, C)
 
 
-def test_checker_catches_an_area_that_is_still_read():
+def test_the_model_catches_an_area_that_is_still_read():
     # the chunk's own state written before S^T q has read the area
     P, C = walk_programs(6)
     P["U"] = [s for s in P["U"] if not (s[0] == "wait" and s[1][0] == "s_read")]
     assert _caught(P, C)
 
 
-def test_checker_catches_scores_over_unread_outputs():
+def test_the_model_catches_scores_over_unread_outputs():
     P, C = walk_programs(6)
     P["S"] = [s for s in P["S"] if not (s[0] == "wait" and s[1][0] == "o_empty")]
     assert _caught(P, C)
 
 
-def test_checker_catches_a_single_state_barrier():
+def test_the_model_catches_a_single_state_barrier():
     # one barrier for the state of every chunk: it may be two completions ahead
     P, C = walk_programs(8, turn=1)
     for r, prog in P.items():

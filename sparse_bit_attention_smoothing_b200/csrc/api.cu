@@ -892,7 +892,8 @@ int sagesla_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void*
 
 // ------------------------------------------- linear attention with a decay
 int sagesla_linear_decay_workspace(int B, int N, int H, int d, long long* bytes)try {
-  if (!bytes || B < 1 || N < 1 || H < 1 || (long long)B * H > 65535 || (d != 64 && d != 128)) return SAGESLA_ERR_INVALID;
+  if (!bytes || B < 1 || N < 1 || N > (1 << 30) || H < 1 || (long long)B * H > 65535 || (d != 64 && d != 128))
+    return SAGESLA_ERR_INVALID;
   int dev = 0;
   SAGESLA_TRY(check_device(&dev));
   const int nseg = linear_decay_segments(B, N, H, sm_count(dev));

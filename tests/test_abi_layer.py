@@ -194,3 +194,9 @@ def t(*shape, dtype=torch.bfloat16):
 def test_binding_refuses(sg, call):
     with pytest.raises(ValueError):
         call(sg)
+
+
+@pytest.mark.parametrize("N", [(1 << 30) + 1, (1 << 31) - 1])
+def test_linear_decay_workspace_too_long(sg, N):
+    n = LL(0)
+    assert sg.lib().sagesla_linear_decay_workspace(1, N, 1, 64, ctypes.byref(n)) == INVALID

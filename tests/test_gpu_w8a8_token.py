@@ -183,3 +183,21 @@ def test_other_stream_and_captured(sg, M):
     assert torch.equal(outs[0], want)
     assert torch.equal(outs[1], sg.sagesla_w8a8_token_linear(xs[1], wq, sw, bias=b))
     assert sg.sync_status() == 0
+
+
+@pytest.mark.parametrize("N,K", [(5120, 5120), (77, 16), (129, 144), (1000, 1168), (300, 13824), (40000, 5120), (130, 131056)])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9])
+def test_linear_is_quantiser_and_product(sg, M, N, K):
+    # one call of the layer: the same bits as its two halves, special rows too
+    x, w, b = inputs(M, N, K, HF if M % 2 else BF, M + K)
+    if M > 2:
+        x[1] = 0
+        x[2, K - 1] = float("nan")
+    if M > 4:
+        x[3] = 2.0 ** -20 if x.dtype == HF else 2.0 ** -110
+        x[4, 0] = float("inf")
+    wq, sw = sg.sagesla_w8a8_token_quant(w)
+    xq, sx = sg.sagesla_w8a8_token_quant(x)
+    want = sg.sagesla_w8a8_token_gemm(xq, sx, wq, sw, bias=b, dtype=x.dtype)
+    got = sg.sagesla_w8a8_token_linear(x, wq, sw, bias=b)
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))

@@ -4,6 +4,8 @@
 // few microseconds, so this layer is compiled (18 us a call in Python, 6 here).
 // Work runs on the current stream of the tensors' device.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
@@ -64,9 +66,12 @@ void vector(const Tensor& t, int64_t n, at::ScalarType type, const char* what) {
        " vector of ", n);
 }
 
+// Both on the current stream of the current device, from torch's allocator and
+// past its dispatcher (two outputs: 6.1 -> 5.8 us a call, one and a workspace: 7.6 -> 7.3).
 Tensor make(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
-  return at::empty(shape, like.options().dtype(type).requires_grad(false));
+  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
+c10::DataPtr scratch(int64_t bytes) { return c10::cuda::CUDACachingAllocator::get()->allocate((size_t)bytes); }
 
 // ------------------------------------------------- W8A8, per token/channel
 py::tuple w8a8_token_quant(const Tensor& a) {
@@ -124,9 +129,9 @@ Tensor w8a8_token_linear(const Tensor& x, const Tensor& wq, const Tensor& sw, co
   Tensor out = token_out(y, M, N, x.scalar_type(), x);
   long long bytes = 0;
   check(sagesla_w8a8_token_workspace(small(M, "M"), small(K, "K"), &bytes), "sagesla_w8a8_token_linear");
-  Tensor ws = make({bytes}, at::kByte, x);
+  const c10::DataPtr ws = scratch(bytes);
   check(sagesla_w8a8_token_linear(ptr(x), x.stride(0), (const int8_t*)ptr(wq), (const float*)ptr(sw), ptr(bias),
-                                  ptr(out), dt, (int)M, small(N, "N"), (int)K, ptr(ws), bytes, here.st),
+                                  ptr(out), dt, (int)M, small(N, "N"), (int)K, ws.get(), bytes, here.st),
         "sagesla_w8a8_token_linear");
   return out;
 }
@@ -222,13 +227,13 @@ py::tuple qk_norm_rope_bwd(const Tensor& dq_out, const MaybeTensor& dk_out, cons
   Tensor dg = make({2, r.d}, at::kFloat, q);
   long long bytes = 0;
   check(sagesla_qk_norm_rope_bwd_workspace(r.B, r.N, r.Hq, r.Hk, r.d, &bytes), "sagesla_qk_norm_rope_bwd");
-  Tensor ws = make({bytes}, at::kByte, q);
+  const c10::DataPtr ws = scratch(bytes);
   float* g = (float*)ptr(dg);
   const auto s = strides<6>({&dq_out, k ? opt(dk_out) : nullptr, &q, opt(k), &oq, opt(ok)});
   check(sagesla_qk_norm_rope_bwd(ptr(dq_out), k ? ptr(dk_out) : nullptr, ptr(q), ptr(k), ptr(gq), k ? ptr(gk) : nullptr,
                                  (float)eps, (const float*)ptr(cos), (const float*)ptr(sin), (const int32_t*)ptr(pos),
                                  ptr(oq), ptr(ok), g, k ? g + r.d : nullptr, r.dt, r.B, r.N, r.Hq, r.Hk, r.d, r.rot,
-                                 r.T, interleaved, s.data(), ptr(ws), bytes, here.st),
+                                 r.T, interleaved, s.data(), ws.get(), bytes, here.st),
         "sagesla_qk_norm_rope_bwd");
   MaybeTensor gk_out;
   if (k) gk_out = dg[1];
@@ -262,12 +267,12 @@ py::tuple linear_decay(const Tensor& q, const Tensor& k, const Tensor& v, const 
   long long bytes = 0;
   check(sagesla_linear_decay_workspace(small(B, "B"), small(N, "N"), small(H, "H"), small(d, "d"), &bytes),
         "sagesla_linear_decay");
-  Tensor ws;
-  if (bytes) ws = make({bytes}, at::kByte, q);
+  c10::DataPtr ws;
+  if (bytes) ws = scratch(bytes);
   const auto s = strides<4>({&q, &k, &v, &o});
   check(sagesla_linear_decay(ptr(q), ptr(k), ptr(v), (const float*)ptr(log_decay), (const float*)ptr(state),
                              (const int32_t*)ptr(lens), (float)scale, ptr(o), (float*)ptr(so), (int)B, (int)N, (int)H,
-                             small(Hk, "H"), (int)d, s.data(), bytes ? ptr(ws) : nullptr, bytes, here.st),
+                             small(Hk, "H"), (int)d, s.data(), ws.get(), bytes, here.st),
         "sagesla_linear_decay");
   return py::make_tuple(head_major ? o.transpose(1, 2) : o, so);
 }

@@ -896,8 +896,8 @@ int sagesla_linear_decay_workspace(int B, int N, int H, int d, long long* bytes)
     return SAGESLA_ERR_INVALID;
   int dev = 0;
   SAGESLA_TRY(check_device(&dev));
-  const int nseg = linear_decay_segments(B, N, H, sm_count(dev));
-  *bytes = nseg > 1 ? (long long)B * H * nseg * d * d * (long long)sizeof(float) : 0;
+  *bytes = (long long)B * H * linear_decay_slots(linear_decay_segments(B, N, H, sm_count(dev))) * d * d *
+           (long long)sizeof(float);
   return SAGESLA_OK;
 } SAGESLA_NO_THROW
 

@@ -16,8 +16,8 @@
 // (2^-16 of the value is left), l^{n-1-j} v_j, which ends in the fp32 state, in
 // three (2^-24).
 //
-// HBM would allow 65 us at 12 heads of 32760 tokens of 128 (4 rows of d a token
-// and head); 158 us measured.  Bound by latency: a chunk is 540 ns of an SM's
+// HBM would allow 62 us at 12 heads of 32760 tokens of 128 (4 rows of d a token
+// and head); 157 us measured.  Bound by latency: a chunk is 540 ns of an SM's
 // share of HBM and 1700 cycles of the tensor pipe, but 4300 cycles (2.35 us)
 // from one to the next, in which every step waits for another one: parts of v
 // (2900 cycles of a warpgroup), products, the state (1650), S^T q, outputs (1300
@@ -33,7 +33,10 @@
 // Few heads do not fill the SMs, so a long sequence is cut into segments: a
 // first launch sums each segment's own state, a second one carries the states
 // across the segments, the third walks each segment from its state.  That reads
-// k and v twice.
+// k and v twice.  Up to kFold segments the walk carries the states itself, one
+// launch less: 48 heads of 1000 tokens (d = 64, 3 segments) 31 -> 27 us; with
+// 4 segments of d = 128 it is even, with 6 it takes 70 us and not 57 (a CTA
+// reads up to 5 states one after another).
 #include <cuda.h>
 
 #include "common.cuh"
@@ -75,7 +78,7 @@ struct Lay {
   static constexpr int third = stages * stage;               // walk: the third part of v [tokens][channels]
   static constexpr int pbuf = third + (kOut ? tile : 0);     // two of P' in two parts
   static constexpr int misc = pbuf + (kOut ? 4 * kBlk : 0);
-  static constexpr int bytes = misc + 2560 + 1024;
+  static constexpr int bytes = misc + 2816 + 1024;
 };
 constexpr int kThreads = 768;
 // Registers of the six warpgroups (copies and MMAs, state, state, parts of v,
@@ -83,6 +86,7 @@ constexpr int kThreads = 768;
 constexpr int kRegs = 80, kRegsIssue = 40, kRegsState = 112, kRegsParts = 72, kRegsP = 72, kRegsOut = 72;
 static_assert(kRegsIssue + 2 * kRegsState + kRegsParts + kRegsP + kRegsOut <= 6 * kRegs, "registers");
 constexpr int kMaxSegments = 256;  // a thread of the carry's CTA for each
+constexpr int kFold = 3;           // see above
 
 __device__ __forceinline__ uint64_t desc_mn(const void* p, uint32_t block_stride) {  // MN-major, 128-byte swizzle
   uint64_t d = (uint64_t)((smem_u32(p) >> 4) & 0x3FFF);
@@ -181,11 +185,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t p_full[2], s_full[2], s_read[2], pp_full[2], pp_empty[2], o_full, o_empty[2], fin;
     // l^m and scale l^m (twice, 16 banks apart) at kC + m, m <= kC; zeros before them
     float power[2 * kC + 16], out_power[2][2 * kC + 16];
+    float whole[kFold];  // l^tokens of the segments, where the walk carries
     int bad[128];  // per channel of v: the segment's first token that is not finite
     uint32_t tmem;
     int abort;
   };
-  static_assert(sizeof(Misc) <= 2560 && L::bytes <= 227 * 1024, "shared memory");
+  static_assert(sizeof(Misc) <= 2816 && L::bytes <= 227 * 1024, "shared memory");
   Misc* ms = reinterpret_cast<Misc*>(smem + L::misc);
   volatile int* abort = &ms->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -223,6 +228,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     ms->power[kC + m] = f;
     ms->out_power[0][kC + m] = ms->out_power[1][kC + m] = a.scale * f;
     if (m < kC) ms->power[m] = ms->out_power[0][m] = ms->out_power[1][m] = 0.f;
+  }
+  constexpr bool kAlone = kOut && kParts == 3;  // one segment
+  const bool fold = !kAlone && a.slots > a.nseg;
+  if (kOut && fold && threadIdx.x >= 256 && threadIdx.x < 256 + a.nseg) {
+    const int i = threadIdx.x - 256, n = max(0, min(len - i * a.seg_tokens, a.seg_tokens));
+    ms->whole[i] = n ? (float)exp((double)__ldg(a.log_decay + h) * n) : 1.f;
   }
   if (warp == 1) tmem_alloc(&ms->tmem, 512);
   tc_fence_before();
@@ -475,15 +486,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kb = (warp >> 3) * KD;        // first channel of k
     const bool mine = ch < D;
     float S[KD];
-    if (kOut) {
-      wait_previous();  // the carried states (all else is the caller's)
-      const float* s0 = a.nseg > 1 ? a.ws + (bh * a.nseg + seg) * D * D : a.state_in ? a.state_in + bh * D * D : nullptr;
-#pragma unroll
-      for (int k = 0; k < KD; ++k) S[k] = s0 && mine ? s0[(size_t)(kb + k) * D + ch] : 0.f;
-    } else {
-#pragma unroll
-      for (int k = 0; k < KD; ++k) S[k] = 0.f;
+    // Where the walk carries (fold): slot 0 of the workspace is a copy of the
+    // state before the first token (state_out may be state_in), slot i + 1
+    // segment i's own state, of the first one what leaves it.
+    float* ws = a.ws + bh * a.slots * D * D + (size_t)kb * D + ch;
+    const float* s0 = a.state_in && mine ? a.state_in + bh * D * D + (size_t)kb * D + ch : nullptr;
+    if (kAlone) {
+    } else if (kOut) {
+      wait_previous();  // the segments' states (all else is the caller's)
+      s0 = !mine || (fold && !seg && !a.state_in) ? nullptr : ws + (size_t)(fold ? min(seg, 1) : seg) * D * D;
+    } else if (!fold || seg) {
+      s0 = nullptr;
     }
+#pragma unroll
+    for (int k = 0; k < KD; ++k) S[k] = s0 ? s0[(size_t)k * D] : 0.f;
+    if (!kOut && s0) {
+#pragma unroll
+      for (int k = 0; k < KD; ++k) ws[(size_t)k * D] = S[k];
+    }
+    if (kOut && fold && mine)
+      for (int i = 1; i < seg; ++i) {
+        const float* u = ws + (size_t)(i + 1) * D * D;
+#pragma unroll
+        for (int k = 0; k < KD; ++k) S[k] = __fmaf_rn(S[k], ms->whole[i], u[(size_t)k * D]);
+      }
     auto put_state = [&](int c) {  // S^T in two bf16 parts, the A operand of chunk c's S^T q
       const uint32_t to = tmem + quad + s_col(c) + kb;
 #pragma unroll
@@ -504,6 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ms->s_full[c & 1]);
     };
     if (kOut && nc) put_state(0);
+    if (kOut && fold && mine && seg == a.nseg - 1 && a.state_out) {  // the last segment's state in fp32, as the others'
+      float* to = a.state_out + bh * D * D + (size_t)kb * D + ch;
+      const float* u = ws + (size_t)a.nseg * D * D;
+#pragma unroll
+      for (int k = 0; k < KD; ++k) to[(size_t)k * D] = __fmaf_rn(S[k], ms->whole[seg], u[(size_t)k * D]);
+    }
     for (int c = 0; c < nc; ++c) {
       ok = all(mbar_wait(&ms->u_full[c & 1], (c / 2) & 1, abort, wd));
       if (!ok) break;
@@ -524,12 +556,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (kOut && c + 1 < nc) put_state(c + 1);
     }
-    float* to = kOut ? (a.nseg > 1 || !a.state_out ? nullptr : a.state_out + bh * D * D)
-                     : a.ws + (bh * a.nseg + seg) * D * D;
+    float* to = !kOut ? ws + (size_t)(seg + fold) * D * D
+                : kAlone && a.state_out ? a.state_out + bh * D * D + (size_t)kb * D + ch : nullptr;
     if (to && mine) {
       const bool nan = *reinterpret_cast<volatile int*>(&ms->bad[ch]) != INT32_MAX;
 #pragma unroll
-      for (int k = 0; k < KD; ++k) to[(size_t)(kb + k) * D + ch] = nan ? __int_as_float(0x7fffffff) : S[k];
+      for (int k = 0; k < KD; ++k) to[(size_t)k * D] = nan ? __int_as_float(0x7fffffff) : S[k];
     }
   } else if (warp >= 12 && warp < (kOut ? 16 : 20)) {
     // ------------------------------ parts of v ----------------------------
@@ -660,8 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Across the segments of a (sequence, head): the state before each one in the
-// place of its own state, and the last one out.  An element a thread.
+// More than kFold segments: across those of a (sequence, head), the state
+// before each one in the place of its own state, and the last one out.  An
+// element a thread.
 __global__ void __launch_bounds__(256) linear_decay_carry_kernel(const DecayArgs a) {
   const int dd = a.d * a.d, at = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y, b = blockIdx.z;
   const size_t bh = (size_t)b * a.H + h;
@@ -677,7 +710,7 @@ __global__ void __launch_bounds__(256) linear_decay_carry_kernel(const DecayArgs
   __syncthreads();
   float s = a.state_in ? a.state_in[bh * dd + at] : 0.f;
   wait_previous();
-  float* ws = a.ws + bh * a.nseg * dd + at;
+  float* ws = a.ws + bh * a.slots * dd + at;
   for (int i0 = 0; i0 < a.nseg; i0 += 16) {  // sixteen segments' loads in flight
     float u[16];
 #pragma unroll
@@ -799,7 +832,7 @@ cudaError_t decay_launch(DecayArgs a, int* wd, cudaStream_t st) {
   if (a.nseg == 1) return walk(0, linear_decay_kernel<D, true, 3>, Lay<D, true>::bytes, false);
   cudaError_t e = walk(1, linear_decay_kernel<D, false, 3>, Lay<D, false>::bytes, false);
   if (e != cudaSuccess) return e;
-  if ((e = run(linear_decay_carry_kernel, dim3(D * D / 256, a.H, a.B), 256, 0, true, a)) != cudaSuccess) return e;
+  if (a.slots == a.nseg && (e = run(linear_decay_carry_kernel, dim3(D * D / 256, a.H, a.B), 256, 0, true, a)) != cudaSuccess) return e;
   return walk(2, linear_decay_kernel<D, true, 2>, Lay<D, true>::bytes, true);
 }
 
@@ -808,26 +841,29 @@ cudaError_t decay_launch(DecayArgs a, int* wd, cudaStream_t st) {
 // Segments of a sequence: as many as there are SMs for, where the walk that
 // they shorten is worth the second pass over k and v and two more launches.  In
 // chunks of a walk (2.35 us each): both passes take 1.34 a chunk, the launches
-// and the ends of the kernels 5.  Measured, us with 1 and with s segments: 12
-// heads of 32760 tokens 1204, 160 (12); 8 of 4096 156, 28 (16); 48 of 1000 (d =
-// 64) 36, 31 (3); 2 of 500 20, 10 (8); 48 of 300 18, 33 (3); 80 of 4096 161, 188
+// and the ends of the kernels 5, or 3.5 without the carry's.  Measured, us with 1 and with s segments: 12
+// heads of 32760 tokens 1204, 157 (12); 8 of 4096 156, 28 (16); 48 of 1000 (d =
+// 64) 36, 27 (3); 2 of 500 20, 10 (8); 48 of 300 18, 33 (3); 80 of 4096 161, 188
 // (3: two rounds of CTAs, never taken).
 int linear_decay_segments(int B, int N, int H, int sms) {
   const long heads = (long)B * H, nc = (N + kC - 1) / kC;
   long best = 1;
   double cost = (double)nc;
   for (long s = 2; s <= nc && heads * s <= sms && s <= kMaxSegments; ++s) {
-    const double c = 1.34 * (double)((nc + s - 1) / s) + 5;
+    const double c = 1.34 * (double)((nc + s - 1) / s) + (s <= kFold ? 3.5 : 5);
     if (c < cost) cost = c, best = s;
   }
   const long per = (nc + best - 1) / best;  // chunks of a segment
   return (int)((nc + per - 1) / per);
 }
 
+int linear_decay_slots(int nseg) { return nseg == 1 ? 0 : nseg <= kFold ? nseg + 1 : nseg; }
+
 cudaError_t launch_linear_decay(const DecayArgs& a0, int* wd, cudaStream_t st) {
   DecayArgs a = a0;
   const int nc = (a.N + kC - 1) / kC;
   a.seg_tokens = (nc + a.nseg - 1) / a.nseg * kC;
+  a.slots = linear_decay_slots(a.nseg);
   return a.d == 64 ? decay_launch<64>(a, wd, st) : decay_launch<128>(a, wd, st);
 }
 

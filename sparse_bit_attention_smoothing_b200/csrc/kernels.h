@@ -142,13 +142,14 @@ struct DecayArgs {
   float* state_out = nullptr;        // may be state_in; nullptr: not kept
   const int32_t* lens = nullptr;     // [B], or nullptr: N
   long qs[3] = {}, ks[3] = {}, vs[3] = {}, os[3] = {};  // strides in elements: batch, token, head
-  float* ws = nullptr;               // [B][H][nseg][d][d]: the segments' states (nseg > 1)
+  float* ws = nullptr;               // [B][H][slots][d][d]: the segments' states
   float scale = 1.f;
   int B = 0, N = 0, H = 0, Hk = 0, d = 0;
-  int nseg = 1, seg_tokens = 0;      // segments of a sequence, tokens of each
+  int nseg = 1, seg_tokens = 0, slots = 0;  // segments of a sequence, tokens of each, states in ws
   int step[3][2] = {};               // q, k, v: whether the maps' head and batch coordinates move
 };
 int linear_decay_segments(int B, int N, int H, int sms);
+int linear_decay_slots(int nseg);  // states of the workspace a (sequence, head)
 cudaError_t launch_linear_decay(const DecayArgs& a, int* wd, cudaStream_t st);
 cudaError_t launch_linear_decay_step(const DecayArgs& a, int sms, cudaStream_t st);
 // Waits `probes` times on an mbarrier that never completes, then sets *wd.

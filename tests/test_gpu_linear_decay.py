@@ -181,3 +181,31 @@ def test_other_stream_and_captured(sg, N):
         w = w + sg.sagesla_linear_decay_step(*step, ld, w[1], state_out=torch.empty_like(s))
         assert all(torch.equal(a, b) for a, b in zip(o, w))
     assert sg.sync_status() == 0
+
+
+@pytest.mark.parametrize("B,N,H,Hk,d,segments", [(3, 1000, 16, 4, 64, 3), (6, 1100, 12, 6, 128, 2), (4, 1500, 10, 10, 128, 3)])
+def test_few_segments(sg, B, N, H, Hk, d, segments):
+    """Two and three segments, whose states the walk joins itself: with and without a state, in place, lengths that end in
+    every segment, a v that is not finite."""
+    assert sg.sagesla_linear_decay_workspace(B, N, H, d) == 4 * B * H * (segments + 1) * d * d
+    q, k, v, ld, s = inputs(B, N, H, Hk, d, 17)
+    for state in (s, None):
+        check(sg.sagesla_linear_decay(q, k, v, ld, state, scale=0.1), q, k, v, ld, state, None, 0.1)
+    lens = torch.tensor([0, 1, N // 2, N - 1, N // 4, N][:B], dtype=torch.int32, device="cuda")
+    for b, n in enumerate(lens.tolist()):
+        for t in (q, k, v):
+            t[b, n:] = float("nan")
+    got = sg.sagesla_linear_decay(q, k, v, ld, s, lens=lens, scale=0.1)
+    check(got, *(torch.nan_to_num(t) for t in (q, k, v)), ld, s, lens, 0.1)
+    assert torch.equal(got[1][0], s[0])
+    st = s.clone()
+    o, _ = sg.sagesla_linear_decay(q, k, v, ld, st, lens=lens, scale=0.1, state_out=st)
+    assert torch.equal(st, got[1]) and torch.equal(o, got[0])
+    v[2, N // 2 - 40, 0, 5] = float("inf")
+    o, st = sg.sagesla_linear_decay(q, k, v, ld, s, lens=lens, scale=0.1)
+    of, bad = got[0].clone(), torch.zeros_like(got[0], dtype=torch.bool)
+    bad[2, N // 2 - 40:N // 2, :H // Hk, 5] = True
+    assert torch.isnan(o[bad]).all() and torch.equal(o[~bad], of[~bad])
+    worst = torch.zeros_like(st, dtype=torch.bool)
+    worst[2, :H // Hk, :, 5] = True
+    assert torch.isnan(st[worst]).all() and torch.equal(st[~worst], got[1][~worst])

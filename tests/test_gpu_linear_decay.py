@@ -209,3 +209,35 @@ def test_few_segments(sg, B, N, H, Hk, d, segments):
     worst = torch.zeros_like(st, dtype=torch.bool)
     worst[2, :H // Hk, :, 5] = True
     assert torch.isnan(st[worst]).all() and torch.equal(st[~worst], got[1][~worst])
+
+
+@pytest.mark.parametrize("B,N,H,d", [(3, 700, 16, 64), (1, 2000, 60, 128), (1, 900, 9, 128)])
+def test_segments_captured_in_place(sg, B, N, H, d):
+    """Calls one after another in one graph, each from the state that the one before left in place, replayed on new
+    inputs while another graph of the same calls runs."""
+    q, k, v, ld, s = inputs(B, N, H, H, d, 31)
+    lens = torch.tensor([N, N // 2, 3][:B], dtype=torch.int32, device="cuda")
+    sets = []
+    for i in range(2):
+        qi, st = q.clone(), s.clone()
+        sg.sagesla_linear_decay(qi, k, v, ld, st, lens=lens, state_out=st)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = [sg.sagesla_linear_decay(qi, k, v, ld, st, lens=lens, scale=0.1, state_out=st)[0] for _ in range(3)]
+        sets.append((g, qi, st, outs))
+    for i, (g, qi, st, outs) in enumerate(sets):
+        qi.copy_(q.flip(1) if i else q * 2)
+        st.copy_(s)
+    torch.cuda.synchronize()
+    for g, *_ in sets:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            g.replay()
+    torch.cuda.synchronize()
+    for g, qi, st, outs in sets:
+        w = s
+        for o in outs:
+            want, w = sg.sagesla_linear_decay(qi, k, v, ld, w, lens=lens, scale=0.1)
+            assert torch.equal(o, want)
+        assert torch.equal(st, w)
+    assert sg.sync_status() == 0

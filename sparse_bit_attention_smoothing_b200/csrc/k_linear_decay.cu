@@ -9,8 +9,8 @@
 // Only powers of l from 0 to 64 occur, so nothing overflows.
 //
 // Every product runs on the tensor cores with fp32 sums, transposed so that
-// the channels of v are the MMA's rows: a thread then owns one row of the
-// state (its channel of v, all channels of k) in fp32 registers, and S and P'
+// the channels of v are the MMA's rows: a thread then owns half a row of the
+// state (its channel of v, half of those of k) in fp32 registers, and S and P'
 // never need a transposition.  What is not bf16 by itself is held in bf16
 // parts whose sum is it: P' and S, which end in a bf16 output, in two parts
 // (2^-16 of the value is left), l^{n-1-j} v_j, which ends in the fp32 state, in
@@ -35,8 +35,8 @@
 // across the segments, the third walks each segment from its state.  That reads
 // k and v twice.  Up to kFold segments the walk carries the states itself, one
 // launch less: 48 heads of 1000 tokens (d = 64, 3 segments) 31 -> 27 us; with
-// 4 segments of d = 128 it is even, with 6 it takes 70 us and not 57 (a CTA
-// reads up to 5 states one after another).
+// 4 segments (d = 64) it is even, with 6 (d = 128) 24 heads of 4096 take 70 us
+// and not 57 (a CTA reads up to 5 states one after another).
 #include <cuda.h>
 
 #include "common.cuh"

@@ -32,7 +32,10 @@
  * Conventions for every entry point:
  *   - Tensors are DEVICE pointers owned by the caller, bf16, contiguous
  *     [B][H][N][d], 16-byte aligned.  Inputs are never written; rows n >= N
- *     are never read or written.
+ *     are never read or written.  The attention, its parity entries and the
+ *     block-scaled W8A8 layer ask the runtime for each pointer and answer
+ *     SAGESLA_ERR_POINTER, without launching, for an address that it does not
+ *     know (the operators whose calls take a few microseconds do not ask).
  *   - The call is asynchronous on `stream` (a cudaStream_t; NULL = legacy
  *     default stream).  It performs no host synchronisation, except that the
  *     first call needing a larger workspace on a (device, stream) allocates it
@@ -63,7 +66,8 @@ enum {
   SAGESLA_ERR_OOM = -3,            /* workspace allocation failed */
   SAGESLA_ERR_LAUNCH = -4,         /* a CUDA launch or runtime call failed */
   SAGESLA_ERR_DEVICE_TIMEOUT = -5, /* a bounded device-side wait gave up */
-  SAGESLA_ERR_NO_DEVICE = -6       /* current device is not sm_100 */
+  SAGESLA_ERR_NO_DEVICE = -6,      /* current device is not sm_100 */
+  SAGESLA_ERR_POINTER = -7         /* a pointer is no memory of a device, managed or page-locked */
 };
 
 /*

@@ -18,7 +18,8 @@ LIB_PATH = os.path.join(_HERE, "libsagesla.so")
 _lib = None
 
 ERRORS = {0: "ok", -1: "invalid argument", -2: "misaligned pointer", -3: "out of memory",
-          -4: "CUDA launch error", -5: "device watchdog timeout", -6: "not an sm_100 device"}
+          -4: "CUDA launch error", -5: "device watchdog timeout", -6: "not an sm_100 device",
+          -7: "a pointer is not memory of a device"}
 
 
 class SageSLAError(RuntimeError):

@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -149,6 +150,22 @@ int validate(const void* q, const void* k, const void* v, const void* out, int B
   const int nb = (N + block - 1) / block;
   if (sagesla::pool_topk_smem(nb) > 227 * 1024) return SAGESLA_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return SAGESLA_ERR_MISALIGNED;
+  return SAGESLA_OK;
+}
+
+// Whether every pointer (nullptr: an argument that is not given) is memory that
+// the runtime knows: of a device, managed or page-locked.  An address that is
+// none of these would end in a memory fault on the GPU, and with it the context.
+int known_memory(std::initializer_list<const void*> ps) {
+  for (const void* p : ps) {
+    if (!p) continue;
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+      cudaGetLastError();
+      return SAGESLA_ERR_POINTER;
+    }
+    if (at.type == cudaMemoryTypeUnregistered) return SAGESLA_ERR_POINTER;
+  }
   return SAGESLA_OK;
 }
 
@@ -302,6 +319,7 @@ int run_attn(const void* q, const void* k, const void* v, const void* proj_w, vo
   if (proj_w && !aligned16(proj_w)) return SAGESLA_ERR_MISALIGNED;
   int dev = 0;
   SAGESLA_TRY(check_device(&dev));
+  SAGESLA_TRY(known_memory({q, k, v, out, proj_w, nrm ? nrm->gq : nullptr, nrm ? nrm->gk : nullptr}));
   Geom g = make_geom(B, H, N, block, topk);
   g.tok = tok;
   const bool dense = g.kc == g.nb;
@@ -680,6 +698,7 @@ int sagesla_get_quant(const void* q, const void* k, const void* v, int B, int H,
   if (!k8 || !v8 || !sq || !sk || !sv || !mu) return SAGESLA_ERR_INVALID;
   int dev = 0;
   SAGESLA_TRY(check_device(&dev));
+  SAGESLA_TRY(known_memory({q, k, v, q8, k8, v8, sq, sk, sv, mu}));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const Geom g = make_geom(B, H, N, 64, 1.0f);
   const Buffers sizes = carve(nullptr, g);
@@ -708,6 +727,7 @@ int sagesla_get_mask(const void* q, const void* k, int B, int H, int N, int d, i
   SAGESLA_TRY(validate(q, k, k, idx_out, B, H, N, d, block, topk));
   int dev = 0;
   SAGESLA_TRY(check_device(&dev));
+  SAGESLA_TRY(known_memory({q, k, idx_out, qbar, kbar}));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const Geom g = make_geom(B, H, N, block, topk);
   const Buffers sizes = carve(nullptr, g);
@@ -745,6 +765,7 @@ int sagesla_w8a8_quant(const void* a, int rows, int cols, void* codes, float* sc
   if (!aligned16(a) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u)) return SAGESLA_ERR_MISALIGNED;
   int dev = 0;
   SAGESLA_TRY(check_device(&dev));
+  SAGESLA_TRY(known_memory({a, codes, scales}));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(9, st);
   return launch_rc(launch_w8a8_quant(a, rows, cols, static_cast<uint8_t*>(codes), scales, st));
@@ -756,6 +777,7 @@ int sagesla_w8a8_gemm(const void* xq, const float* sx, const void* wq, const flo
   SAGESLA_TRY(check_gemm(xq, sx, wq, sw, y, M, N, K));
   int dev = 0;
   SAGESLA_TRY(check_device(&dev));
+  SAGESLA_TRY(known_memory({xq, sx, wq, sw, y}));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(10, st);
   return launch_rc(launch_w8a8_gemm(static_cast<const uint8_t*>(xq), sx, static_cast<const uint8_t*>(wq), sw, y, M, N,
@@ -769,6 +791,7 @@ int sagesla_w8a8_linear(const void* x, const void* wq, const float* sw, void* y,
   SAGESLA_TRY(check_gemm(x, &one, wq, sw, y, M, N, K));  // x stands in for its codes in the checks
   int dev = 0;
   SAGESLA_TRY(check_device(&dev));
+  SAGESLA_TRY(known_memory({x, wq, sw, y}));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t cb = up(w8a8_codes_bytes(M, K));
   uint8_t* base = nullptr;
@@ -972,6 +995,7 @@ const char* sagesla_strerror(int code) {
     case SAGESLA_ERR_OOM: return "workspace allocation failed";
     case SAGESLA_ERR_LAUNCH: return "CUDA launch or runtime error";
     case SAGESLA_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait gave up";
+    case SAGESLA_ERR_POINTER: return "a pointer is no memory of a device, managed or page-locked";
     case SAGESLA_ERR_NO_DEVICE: return "current device is not an sm_100 GPU";
     default: return "unknown error";
   }

@@ -468,12 +468,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qk_norm_rope_bwd_kernel(const 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u >= pass) break;
-      const float rv = r.take(u, L);
+      // A lane without this head has zeros, whose norm without eps is infinite: it adds 0.
+      const float rt = r.take(u, L), rv = u < heads ? rt : 0.f;
       const uint64_t rr = both(rv), k = both(-(rv * (m.take(u, L) * a.inv_d)) * rv * rv);  // in this order: no overflow
       const Part<P> f = in.get(u), gs = mul_part(g[u], rr);
       Part<P> y = mul_part(gs, gm);
 #pragma unroll
-      for (int i = 0; i < 4 * P; ++i) {  // (a lane without this head has zeros)
+      for (int i = 0; i < 4 * P; ++i) {
         sums.r[i / 4].e[i % 4] = f32x2_fma(gs.r[i / 4].e[i % 4], f.r[i / 4].e[i % 4], sums.r[i / 4].e[i % 4]);
         y.r[i / 4].e[i % 4] = f32x2_fma(f.r[i / 4].e[i % 4], k, y.r[i / 4].e[i % 4]);
       }

@@ -269,6 +269,14 @@ __device__ __forceinline__ bool elect_one() {
 // are visible (at once, where the launch had no such attribute).
 __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A value that the kernel before this one wrote, behind wait_previous.  Not
+// __ldg: the read-only path is for memory that nobody writes while the kernel
+// is resident, and this kernel may be resident before the write.
+__device__ __forceinline__ float ld_previous(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
 
 // ------------------------------ CTA pairs --------------------------------
 // Two CTAs of a cluster share one MMA (cta_group::2): rank 0, the leader,

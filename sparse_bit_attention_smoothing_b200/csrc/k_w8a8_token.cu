@@ -173,7 +173,7 @@ __device__ __forceinline__ void rows_out(const uint8_t* o, uint16_t* y, int row0
 template <int kType>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     w8a8_token_gemm_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
-                           const __grid_constant__ CUtensorMap my, const float* __restrict__ sx,
+                           const __grid_constant__ CUtensorMap my, const float* sx,
                            const float* __restrict__ sw, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y,
                            int M, int N, int K, int BN, int tma_out, int* wd) {
   constexpr int S = kStages, SB = kStageBytes, kBM = 256;
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         ws[c] = in ? __ldg(sw + n0 + c) : 0.f;
         ws[kMaxBN + c] = in && bias ? widen1<kType>(__ldg(bias + n0 + c)) : 0.f;
       }
-      const float rs = row0 + lane < M ? __ldg(sx + row0 + lane) : 0.f;
+      const float rs = row0 + lane < M ? ld_previous(sx + row0 + lane) : 0.f;
       __syncwarp();
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->acc_full[buf], (tl >> 1) & 1, abort, wd));
       tc_fence_after();
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 template <int kType>
 __global__ void __launch_bounds__(kGemmThreads)
     w8a8_token_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
-                          const float* __restrict__ sx, const float* __restrict__ sw,
+                          const float* sx, const float* __restrict__ sw,
                           const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int M, int N, int K, int BN,
                           int S, int splits, int* wd) {
   extern __shared__ uint8_t smem_raw[];
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kGemmThreads)
     }
 #pragma unroll
     for (int r = 0; r < kMaxSplits - 1; ++r) s.x += o[r].x, s.y += o[r].y, s.z += o[r].z, s.w += o[r].w;
-    const float rs = __ldg(sx + c);
+    const float rs = ld_previous(sx + c);
     const float f0 = __fmaf_rn(__fmul_rn((float)s.x, rs), s4[0], b4[0]), f1 = __fmaf_rn(__fmul_rn((float)s.y, rs), s4[1], b4[1]);
     const float f2 = __fmaf_rn(__fmul_rn((float)s.z, rs), s4[2], b4[2]), f3 = __fmaf_rn(__fmul_rn((float)s.w, rs), s4[3], b4[3]);
     const uint32_t lo = pack2<kType>(f0, f1), hi = pack2<kType>(f2, f3);

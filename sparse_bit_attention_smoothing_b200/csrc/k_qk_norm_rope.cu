@@ -46,10 +46,10 @@ __device__ __forceinline__ Piece<T> load8(const T* p) {
   return r;
 }
 template <typename T>
-__device__ __forceinline__ Piece<T> zero8() {
+__device__ __forceinline__ Piece<T> fill8(uint32_t w) {
   Piece<T> r;
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = make_uint4(w, w, w, w);
   return r;
 }
 __device__ __forceinline__ void widen(const Piece<__nv_bfloat16>& p, float (&f)[8]) {
@@ -318,11 +318,11 @@ struct Group {
 template <typename T, int P, int U>
 struct Rows {
   Piece<T> v[U][P];
-  __device__ __forceinline__ void load(const T* p, const Place<P>& pl, long step, int heads) {
+  __device__ __forceinline__ void load(const T* p, const Place<P>& pl, long step, int heads, uint32_t none = 0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) v[u][i] = u < heads ? load8(p + 8 * pl.at[i]) : zero8<T>();
+      for (int i = 0; i < P; ++i) v[u][i] = u < heads ? load8(p + 8 * pl.at[i]) : fill8<T>(none);
       p += step;
     }
   }
@@ -428,6 +428,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qk_norm_rope_bwd_kernel(const 
   const int pass = a.pass[grp.tsr], heads = pl.mine ? grp.heads : 0;
   const long R = 32 / L, xstep = R * t.xs[2], gstep = R * t.dys[2], ystep = R * t.ys[2];
   launch_next();
+  // A place without a head must not have a row of zeros: without eps its norm is
+  // infinite, and 0 * inf would be in dgamma.  With one piece a lane its x is
+  // about one (in all three types; g is 0), with two its factor is dropped: 0.5
+  // and 0.7 % of the time, each the other way round 1.5 %.
+  const uint32_t none = P == 1 && pl.mine ? 0x3f803f80u : 0;
   const Part<P> gm = load_part(static_cast<const T*>(t.gamma), pl);
   Part<P> sums = {};
   const unsigned first = w / (unsigned)a.G;
@@ -435,7 +440,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qk_norm_rope_bwd_kernel(const 
   for (unsigned token = first; token < (unsigned)a.tokens && first < (unsigned)a.stride; token += (unsigned)a.stride) {
     const unsigned b = one ? 0 : token / (unsigned)a.N, n = token - b * (unsigned)a.N;
     Rows<T, P, U> in, gr;
-    in.load(static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[1] + grp.h0 * t.xs[2], pl, xstep, heads);
+    in.load(static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[1] + grp.h0 * t.xs[2], pl, xstep, heads, none);
     gr.load(static_cast<const T*>(t.dy) + b * t.dys[0] + n * t.dys[1] + grp.h0 * t.dys[2], pl, gstep, heads);
     T* dx = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[1] + grp.h0 * t.ys[2];
     const long p = a.pos ? (long)__ldg(a.pos + token) : n;
@@ -468,13 +473,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qk_norm_rope_bwd_kernel(const 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u >= pass) break;
-      // A lane without this head has zeros, whose norm without eps is infinite: it adds 0.
-      const float rt = r.take(u, L), rv = u < heads ? rt : 0.f;
+      const float rt = r.take(u, L), rv = P == 1 || u < heads ? rt : 0.f;
       const uint64_t rr = both(rv), k = both(-(rv * (m.take(u, L) * a.inv_d)) * rv * rv);  // in this order: no overflow
       const Part<P> f = in.get(u), gs = mul_part(g[u], rr);
       Part<P> y = mul_part(gs, gm);
 #pragma unroll
-      for (int i = 0; i < 4 * P; ++i) {
+      for (int i = 0; i < 4 * P; ++i) {  // (where there is no head g is 0)
         sums.r[i / 4].e[i % 4] = f32x2_fma(gs.r[i / 4].e[i % 4], f.r[i / 4].e[i % 4], sums.r[i / 4].e[i % 4]);
         y.r[i / 4].e[i % 4] = f32x2_fma(f.r[i / 4].e[i % 4], k, y.r[i / 4].e[i % 4]);
       }

@@ -411,12 +411,15 @@ __global__ void __launch_bounds__(32 * kWarps, P == 1 ? 3 : 2) qk_norm_rope_kern
 }
 
 // ---------------------------------------------------------------- backward --
-// Persistent: warp w keeps its head group w % G and walks the tokens w / G,
-// w / G + stride, ..., so its lanes hold the running dgamma of their
-// channels in fp32 registers.  The sums of a CTA's warps are joined in shared
-// memory in a fixed order and written as one partial row of q and one of k;
-// dgamma_kernel adds the CTAs' rows in fp64, again in a fixed order: no
-// atomics, the same bits every time.
+// Warp w keeps its head group w % G and walks the tokens w / G, w / G + stride,
+// ..., so its lanes hold the running dgamma of their channels in fp32
+// registers: over kMostTokens tokens of at most 4 rows each, so that the error
+// does not grow with the tokens (more of them are more rounds of CTAs: 720p x
+// 40 heads 839 -> 843 us; sums taken to fp64 in shared memory every 32 tokens
+// cost 1 % with one piece a lane and 7 % with two).  The sums of a CTA's warps
+// are joined in shared memory in a fixed order and written as one partial row
+// of q and one of k; dgamma_kernel adds the CTAs' rows in fp64, again in a
+// fixed order: no atomics, the same bits every time.
 template <typename T, int P, int U>
 __global__ void __launch_bounds__(32 * kWarps, 2) qk_norm_rope_bwd_kernel(const RopeArgs a) {
   __shared__ float part[kWarps][256];
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(256) dgamma_kernel(const float* part, int rows
 
 namespace {
 
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 2, kMostTokens = 128;
 
 template <typename T, int P>
 cudaError_t rope_launch(const RopeArgs& a0, bool back, int sms, cudaStream_t st) {
@@ -578,10 +581,12 @@ cudaError_t rope_launch(const RopeArgs& a0, bool back, int sms, cudaStream_t st)
 }  // namespace
 
 // CTAs of the backward pass: enough for every (token, group) pair or two an
-// SM, and at least one warp a group.
+// SM, and at least one warp a group.  Where a warp would walk more than
+// kMostTokens, as many rounds of two an SM as leave it no more.
 int rope_bwd_ctas(long tokens, int G, int sms) {
-  const long need = (tokens * G + kWarps - 1) / kWarps;
-  long ctas = need < (long)kCtasPerSm * sms ? need : (long)kCtasPerSm * sms;
+  const long full = (long)kCtasPerSm * sms, need = (tokens * G + kWarps - 1) / kWarps;
+  const long rounds = (need + full * kMostTokens - 1) / (full * kMostTokens);
+  const long ctas = need < full ? need : full * rounds;
   const long least = ((long)G + kWarps - 1) / kWarps;
   return (int)(ctas > least ? ctas : least);
 }

@@ -298,7 +298,7 @@ def sagesla_w8a8_linear(x, wq, sw, N: int, y=None, stream=None):
 # ---- operators of the layer around the attention --------------------------
 # These serve single tokens too, whose kernels take a few microseconds, so the
 # checks of the tensors (ValueError), the allocations and the call of the C ABI
-# are compiled (csrc/binding.cpp, _layer.so).  Work runs on `stream` (default:
+# are compiled (csrc/binding.cpp, _layer-*.so).  Work runs on `stream` (default:
 # the current stream of the tensors' device); what a call allocates (its
 # outputs and workspace) is allocated on that stream.
 _layer_mod = None
@@ -311,9 +311,11 @@ def _layer():
 
         import torch  # noqa: F401  (its libraries, before the module that links them)
         lib()
-        path = os.path.join(_HERE, "_layer.so")
+        from . import build
+        path = build.layer_path()
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: run `python -m sparse_bit_attention_smoothing_b200.build`")
+            raise RuntimeError(f"{path} is missing: the binding is not built for this torch and Python, run "
+                               "`python -m sparse_bit_attention_smoothing_b200.build`")
         spec = importlib.util.spec_from_file_location("_layer", path)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)

@@ -15,13 +15,14 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsagesla.so")
-LAYER = os.path.join(PKG, "_layer.so")  # the compiled part of the Python binding (csrc/binding.cpp)
+LAYER_DIR = PKG  # the compiled part of the Python binding (csrc/binding.cpp): _layer-<what it was compiled against>.so
 SOURCES = ["k_prologue.cu", "k_topk.cu", "k_linear.cu", "k_flash.cu", "k_flash64.cu", "k_watchdog.cu", "k_w8a8.cu", "k_w8a8_token.cu", "k_qk_norm_rope.cu",
            "k_linear_decay.cu", "api.cu", "noalloc.cu"]
 HEADERS = ["common.cuh", "kernels.h", "tensormap.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-diag-suppress", "177"]
+LAYER_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-DTORCH_EXTENSION_NAME=_layer", "-DTORCH_API_INCLUDE_EXTENSION_H"]
 
 
 def _nvcc() -> str:
@@ -68,27 +69,48 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
-def build_layer(force: bool = False) -> str:
-    """The compiled binding of the layer operators, against the installed torch and libsagesla.so."""
+def layer_path() -> str | None:
+    """The compiled binding for the torch (its version and where its libraries are), the Python ABI and the flags of now: they
+    are in the file's name, so one that was compiled against others is neither taken for it nor loaded.  None where torch
+    is not installed.  (torch is not imported for it.)"""
+    import hashlib
+    import importlib.metadata
+    import importlib.util
+    import sysconfig
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return None
+    key = [importlib.metadata.version("torch"), os.path.dirname(spec.origin), sysconfig.get_config_var("SOABI"), *LAYER_FLAGS]
+    return os.path.join(LAYER_DIR, "_layer-%s.so" % hashlib.sha256("\n".join(key).encode()).hexdigest()[:12])
+
+
+def build_layer(force: bool = False) -> str | None:
+    """The compiled binding of the layer operators, against the installed torch and libsagesla.so.  Without torch there is
+    nothing to bind to and nothing is built: the C library needs nvcc alone."""
+    layer = layer_path()
+    if layer is None:
+        return None
     src = os.path.join(CSRC, "binding.cpp")
-    if not force and not _stale(LAYER, [src, os.path.join(ROOT, "include", "sagesla.h")]):
-        return LAYER
+    if not force and not _stale(layer, [src, os.path.join(ROOT, "include", "sagesla.h")]):
+        return layer
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension as ext
     inc = [f"-I{p}" for p in ext.include_paths("cuda") + [sysconfig.get_paths()["include"]]]
     libs = [a for p in ext.library_paths("cuda") for a in (f"-L{p}", f"-Wl,-rpath,{p}")]
-    tmp = LAYER + ".tmp%d" % os.getpid()
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-DTORCH_EXTENSION_NAME=_layer",
-           "-DTORCH_API_INCLUDE_EXTENSION_H", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, src,
-           "-o", tmp, f"-L{PKG}", "-lsagesla", "-Wl,-rpath,$ORIGIN", *libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch",
-           "-ltorch_python"]
+    tmp = layer + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("g++") or "g++", *LAYER_FLAGS, f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+           src, "-o", tmp, f"-L{PKG}", "-lsagesla", "-Wl,-rpath,$ORIGIN", *libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
-    os.replace(tmp, LAYER)
-    return LAYER
+    for f in os.listdir(LAYER_DIR):  # those for another torch, Python or flags
+        if f.startswith("_layer") and f.endswith(".so"):
+            os.remove(os.path.join(LAYER_DIR, f))
+    os.replace(tmp, layer)
+    return layer
 
 
 if __name__ == "__main__":

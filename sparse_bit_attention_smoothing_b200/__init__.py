@@ -300,7 +300,8 @@ def sagesla_w8a8_linear(x, wq, sw, N: int, y=None, stream=None):
 # checks of the tensors (ValueError), the allocations and the call of the C ABI
 # are compiled (csrc/binding.cpp, _layer-*.so).  Work runs on `stream` (default:
 # the current stream of the tensors' device); what a call allocates (its
-# outputs and workspace) is allocated on that stream.
+# outputs and workspace) is allocated on that stream.  As the attention's, their
+# results carry no gradient.
 _layer_mod = None
 
 
@@ -366,7 +367,9 @@ def sagesla_qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, pos=None, eps: float 
     [B, N, Hk, d] (k None: q alone) bf16, fp16 or fp32 with any strides (views of a fused projection); gamma_* [d];
     cos, sin fp32 [T, rot/2], the first rot channels turned in pairs (2c, 2c+1) (interleaved) or (c, c + rot/2); pos
     int32 [B, N] (None: the token index; negative: padding, outputs 0).  Returns (q_out, k_out), [B, N, H, d], or
-    [B, H, N, d] as sagesla_attn takes it with head_major; q_out, k_out: [B, N, H, d] views to write to."""
+    [B, H, N, d] as sagesla_attn takes it with head_major; q_out, k_out: [B, N, H, d] views to write to, each exactly its
+    input or apart from both.  Outside autograd: a tensor that requires a gradient is refused, except under torch.no_grad()
+    or in the forward of a torch.autograd.Function, whose backward calls sagesla_qk_norm_rope_bwd."""
     f = _layer().qk_norm_rope
     args = (q, k, gamma_q, gamma_k, cos, sin, pos, eps, interleaved, q_out, k_out, head_major)
     return f(*args) if stream is None else _on(stream, q, f, *args)

@@ -4,6 +4,7 @@
 // few microseconds, so this layer is compiled (18 us a call in Python, 6 here).
 // Work runs on the current stream of the tensors' device.
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -43,6 +44,15 @@ int type_code(const Tensor& t, bool fp32 = false) {
 void same_device(const Tensor& first, std::initializer_list<const Tensor*> others) {
   NEED(first.is_cuda(), "CUDA tensors are needed");
   for (const Tensor* t : others) NEED(!t || t->device() == first.device(), "the tensors are on different devices");
+}
+// The call works outside autograd.  Where a gradient would be wanted of an
+// argument, the results would be cut from its graph without a word.
+void no_gradient(std::initializer_list<const Tensor*> ts, const char* where) {
+  if (!at::GradMode::is_enabled()) return;
+  for (const Tensor* t : ts)
+    NEED(!t || !t->requires_grad(), where,
+         " records no gradient and an argument requires one: call it under torch.no_grad() or in a torch.autograd.Function "
+         "(sagesla_qk_norm_rope_bwd is the backward pass)");
 }
 const Tensor* opt(const MaybeTensor& t) { return t ? &*t : nullptr; }
 void* ptr(const Tensor& t) { return t.data_ptr(); }
@@ -193,6 +203,7 @@ RopeShape rope_shape(const Tensor& q, const MaybeTensor& k, const Tensor& gq, co
 py::tuple qk_norm_rope(const Tensor& q, const MaybeTensor& k, const Tensor& gq, const MaybeTensor& gk,
                        const Tensor& cos, const Tensor& sin, const MaybeTensor& pos, double eps, bool interleaved,
                        const MaybeTensor& q_out, const MaybeTensor& k_out, bool head_major) {
+  no_gradient({&q, opt(k), &gq, k ? opt(gk) : nullptr, &cos, &sin}, "sagesla_qk_norm_rope");
   const RopeShape r = rope_shape(q, k, gq, gk, cos, sin, pos);
   same_device(q, {opt(k), &gq, opt(gk), &cos, &sin, opt(pos), opt(q_out), opt(k_out)});
   Here here(q);
@@ -215,6 +226,7 @@ py::tuple qk_norm_rope_bwd(const Tensor& dq_out, const MaybeTensor& dk_out, cons
                            const Tensor& gq, const MaybeTensor& gk, const Tensor& cos, const Tensor& sin,
                            const MaybeTensor& pos, double eps, bool interleaved, const MaybeTensor& dq,
                            const MaybeTensor& dk) {
+  no_gradient({&dq_out, k ? opt(dk_out) : nullptr, &q, opt(k), &gq, k ? opt(gk) : nullptr, &cos, &sin}, "sagesla_qk_norm_rope_bwd");
   const RopeShape r = rope_shape(q, k, gq, gk, cos, sin, pos);
   const auto type = q.scalar_type();
   NEED(rows4(dq_out, r.B, r.N, r.d, type, "dq_out") == r.Hq, "dq_out must have ", r.Hq, " heads");

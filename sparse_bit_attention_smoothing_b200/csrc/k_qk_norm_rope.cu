@@ -561,7 +561,7 @@ cudaError_t rope_launch(const RopeArgs& a0, bool back, int sms, cudaStream_t st)
     qk_norm_rope_kernel<T, P, U><<<(unsigned)ctas, 32 * kWarps, 0, st>>>(a);
     return cudaGetLastError();
   }
-  const int ctas = rope_bwd_ctas(a.tokens, a.G, sms);
+  const int ctas = (int)rope_bwd_ctas(a.tokens, a.G, sms);  // under 2^23: tokens * G < 2^32
   a.stride = (long)ctas * kWarps / a.G;
   qk_norm_rope_bwd_kernel<T, P, UB><<<ctas, 32 * kWarps, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();
@@ -583,12 +583,12 @@ cudaError_t rope_launch(const RopeArgs& a0, bool back, int sms, cudaStream_t st)
 // CTAs of the backward pass: enough for every (token, group) pair or two an
 // SM, and at least one warp a group.  Where a warp would walk more than
 // kMostTokens, as many rounds of two an SM as leave it no more.
-int rope_bwd_ctas(long tokens, int G, int sms) {
+long rope_bwd_ctas(long tokens, int G, int sms) {
   const long full = (long)kCtasPerSm * sms, need = (tokens * G + kWarps - 1) / kWarps;
   const long rounds = (need + full * kMostTokens - 1) / (full * kMostTokens);
   const long ctas = need < full ? need : full * rounds;
   const long least = ((long)G + kWarps - 1) / kWarps;
-  return (int)(ctas > least ? ctas : least);
+  return ctas > least ? ctas : least;
 }
 
 size_t rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, int sms) {

@@ -123,7 +123,7 @@ struct RopeArgs {
   int d = 0, rot = 0, L = 0, Gq = 0, G = 0, pass[2] = {};
   float eps = 0.f, inv_d = 0.f;
 };
-int rope_bwd_ctas(long tokens, int G, int sms);
+long rope_bwd_ctas(long tokens, int G, int sms);
 size_t rope_bwd_workspace(int B, int N, int Hq, int Hk, int d, int sms);
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, int dtype, bool interleaved, bool back, int sms,
                                 cudaStream_t st);

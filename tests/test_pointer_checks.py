@@ -2,26 +2,12 @@
 sm_100 device, launches counted and not run); on a GPU the same calls are made with host memory."""
 import ctypes
 import os
-import shutil
 import subprocess
 import sys
 
 import pytest
 
-ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-FAKE = os.path.join(ROOT, "_build", "libfake_runtime.so")
-
-
-@pytest.fixture(scope="module")
-def fake():
-    from sparse_bit_attention_smoothing_b200 import build
-    build.build()
-    cc = shutil.which("gcc") or shutil.which("cc")
-    if cc is None:
-        pytest.skip("no C compiler")
-    os.makedirs(os.path.dirname(FAKE), exist_ok=True)
-    subprocess.run([cc, "-O1", "-shared", "-fPIC", os.path.join(ROOT, "tests", "fake_runtime.c"), "-o", FAKE], check=True)
-    return FAKE
+from tests._fake import ROOT, fake  # noqa: F401
 
 
 CALLS = """

@@ -435,7 +435,7 @@ int rope_common(RopeArgs* a, const void* gamma_q, const void* gamma_k, float eps
   if ((double)B * N * ((double)Hq + Hk) >= 4294967296.0) return SAGESLA_ERR_INVALID;
   if (d < 16 || d > 256 || d % 16 != 0 || rot < 0 || rot > d || rot % 16 != 0) return SAGESLA_ERR_INVALID;
   if (T < 1 || (rot && (!cos || !sin)) || (!pos && N > T)) return SAGESLA_ERR_INVALID;
-  if (!aligned16(gamma_q) || !aligned16(gamma_k) || !aligned16(cos) || !aligned16(sin) ||
+  if (!aligned16(gamma_q) || (Hk && !aligned16(gamma_k)) || (rot && (!aligned16(cos) || !aligned16(sin))) ||
       (reinterpret_cast<uintptr_t>(pos) & 3u))
     return SAGESLA_ERR_MISALIGNED;
   a->t[0].gamma = gamma_q;
@@ -900,7 +900,7 @@ int sagesla_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void*
   SAGESLA_TRY(rope_rows(&a.t[0], q, dq_out, dq, strides + 6, strides, strides + 12, dtype, B, N, d));
   if (Hk) SAGESLA_TRY(rope_rows(&a.t[1], k, dk_out, dk, strides + 9, strides + 3, strides + 15, dtype, B, N, d));
   if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(dgamma_q) & 3u) ||
-      (reinterpret_cast<uintptr_t>(dgamma_k) & 3u))
+      (Hk && (reinterpret_cast<uintptr_t>(dgamma_k) & 3u)))
     return SAGESLA_ERR_MISALIGNED;
   int dev = 0;
   SAGESLA_TRY(check_device(&dev));

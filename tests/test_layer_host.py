@@ -38,6 +38,31 @@ for d in (16, 128, 256):
             assert n >= need(1, N, H, 0, d)
 """
 
+IGNORED = """
+i64 = ctypes.c_int64
+odd = P(0x10001)  # what an argument that is not used may be
+s12, s18 = (i64 * 12)(*[1024, 128, 64] * 4), (i64 * 18)(*[1024, 128, 64] * 6)
+def fwd(gk, cos, sin, k, ko, Hk, rot):
+    return L.sagesla_qk_norm_rope(A, k, A, gk, F(1e-6), cos, sin, None, A, ko, 0, 1, 8, 2, Hk, 64, rot, 8, 1, s12, None)
+def bwd(gk, cos, sin, k, dk, dgk, Hk, rot):
+    return L.sagesla_qk_norm_rope_bwd(A, k, A, k, A, gk, F(1e-6), cos, sin, None, A, dk, A, dgk, 0, 1, 8, 2, Hk, 64, rot, 8, 1,
+                                      s18, A, LL(1 << 20), None)
+assert fwd(A, A, A, A, A, 2, 64) == 0 and bwd(A, A, A, A, A, A, 2, 64) == 0
+# used: refused
+assert fwd(odd, A, A, A, A, 2, 64) == -2 and fwd(A, odd, A, A, A, 2, 64) == -2 and fwd(A, A, A, odd, A, 2, 64) == -2
+assert bwd(A, A, A, A, A, odd, 2, 64) == -2
+# not used: whatever they are
+n = fake.fake_launches()
+assert fwd(odd, A, A, odd, odd, 0, 64) == 0 and fwd(A, odd, odd, A, A, 2, 0) == 0
+assert bwd(odd, A, A, odd, odd, odd, 0, 64) == 0 and bwd(A, odd, odd, A, A, A, 2, 0) == 0
+assert fake.fake_launches() == n + 6
+"""
+
+
+def test_unused_arguments_are_ignored(fake):  # noqa: F811
+    """Hk = 0: no k and nothing of it; rot = 0: no tables."""
+    run(fake, IGNORED)
+
 
 def test_backward_workspace_over_all_sizes(fake):  # noqa: F811
     run(fake, WORKSPACE)

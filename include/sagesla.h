@@ -333,9 +333,10 @@ int sagesla_w8a8_token_linear(const void* x, long long ldx, const int8_t* wq, co
 
 /*
  * sagesla_qk_norm_rope: RMS norm of every query and key head and the position
- * rotation, in one pass over q and k (what stands between a DiT's projections
- * and sagesla_attn where the norm is taken per head; sagesla_attn_qknorm is
- * the norm over all heads).  Per row of d channels, in fp32:
+ * rotation, in one pass over q and k: what stands between the projections and
+ * sagesla_attn in models that take the norm of each head.  (The video models of
+ * this library's workloads take it over all heads: sagesla_attn_qknorm, which
+ * has no rotation.)  Per row of d channels, in fp32:
  *   n = x / sqrt(mean(x^2) + eps) * gamma   (gamma_q / gamma_k: [d] of the
  *       tensors' type, shared by the heads),
  *   the first `rot` channels turned in pairs by the token's position p,
@@ -357,7 +358,9 @@ int sagesla_w8a8_token_linear(const void* x, long long ldx, const int8_t* wq, co
  * d a multiple of 16 from 16 to 256, rot a multiple of 16 from 0 to d; eps in
  * [0, 1]; B*N < 2^31, Hq, Hk <= 65535, B*N*(Hq+Hk) < 2^32.  Pointers 16-byte
  * aligned, strides multiples of 16 bytes, not negative, below 2^38 elements;
- * the rows of an output must not overlap.  |x| below 2^60 (squares are summed in fp32).
+ * the rows of an output must not overlap.  |x| below 2^60 (squares are summed in
+ * fp32); with eps = 0 some |x| of a row above 2^-60 (a row of zeros has no norm
+ * then: NaN).
  * Nothing is allocated: the call can be captured.  Codes as sagesla_attn.
  *
  * sagesla_qk_norm_rope_bwd: its backward pass.  dq_out, dk_out: gradients of
@@ -382,9 +385,10 @@ int sagesla_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void*
                              sagesla_stream_t stream);
 
 /*
- * Causal linear attention with a decay for each head: the streaming form of
- * the linear branch, whose sums over tokens become a state that a clip's next
- * tokens continue.  Per sequence b and head h, with key head h / (H/Hk):
+ * Causal linear attention with a decay for each head: sums over the tokens so
+ * far are a state that the next tokens continue.  (It is not a form of the
+ * linear branch above, which sees all tokens, maps q and k by phi and divides
+ * by phi(q) Z; this has neither.)  Per sequence b and head h, with key head h / (H/Hk):
  *   S_t = e^{log_decay[h]} S_{t-1} + k_t v_t^T,   out_t = scale * q_t^T S_t,
  * S [d channels of k][d of v] in fp32; out rounded once to bf16.
  * sagesla_linear_decay: whole prompts.

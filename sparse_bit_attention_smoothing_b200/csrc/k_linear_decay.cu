@@ -17,7 +17,9 @@
 // three (2^-24).
 //
 // HBM would allow 62 us at 12 heads of 32760 tokens of 128 (4 rows of d a token
-// and head); 157 us measured.  Bound by latency: a chunk is 540 ns of an SM's
+// and head).  A call on inputs from HBM takes 188 us, one after another on the
+// same buffers 157; all times in this file but the single tokens' are of the
+// second kind.  Bound by latency: a chunk is 540 ns of an SM's
 // share of HBM and 1700 cycles of the tensor pipe, but 4300 cycles (2.35 us)
 // from one to the next, in which every step waits for another one: parts of v
 // (2900 cycles of a warpgroup), products, the state (1650), S^T q, outputs (1300

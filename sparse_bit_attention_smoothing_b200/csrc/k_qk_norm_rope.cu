@@ -9,6 +9,11 @@
 // Backward, with g = R(p)^T dy, xh = x r, u = g gamma:
 //   dx = r (u - xh mean(u xh)),   dgamma = sum over rows of g xh.
 //
+// Times in this file are of calls one after another on the same buffers, bf16
+// where no type is named.  On other inputs with every call: 75600 tokens x 40/40
+// heads of 128 forward 582 us; 32760 x 12/12 backward 137.  fp32 at 32760 x 12/12
+// from HBM: forward 143 us (5.6 TB/s), backward 205 (5.9 TB/s).
+//
 // Bound by HBM in both directions: a row is read once and written once (the
 // backward pass recomputes r from the x it has to read anyway, so the forward
 // pass saves nothing); what the kernels cost beside the bytes is issue slots.

@@ -4,6 +4,10 @@
 //   s = fl32(amax/127), code = RNE(fl32(x * fl32(127/amax))) per row;
 //   y[m][n] = (integer dot of the codes) * s_x[m] * s_w[n] + bias[n].
 //
+// Times in this file are of kernels one after another on the same buffers, so
+// small operands come from L2.  A call on inputs from HBM, 5120 -> 5120: 1 token
+// 10.2 us, 1024 tokens 33.5, 75600 tokens 1540.
+//
 // The scales leave the sum over K, so the product runs through the whole of K
 // in INT32 (exact for K <= 131056: 2^14 K < 2^31) and the scales, the bias
 // and the one rounding are the epilogue of the output tile.

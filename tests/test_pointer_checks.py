@@ -44,7 +44,7 @@ print("ok", fake.fake_launches())
 """
 
 
-def test_no_launch_on_unknown_addresses(fake):
+def test_no_launch_on_unknown_addresses(fake):  # noqa: F811
     r = subprocess.run([sys.executable, "-c", CALLS % (ROOT, fake)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.startswith("ok"), (r.stdout, r.stderr[-2000:])
 
@@ -57,15 +57,17 @@ def pytest_sessionfinish(session):
 """
 
 
-def test_argument_checks_launch_nothing(fake):
-    """tests/test_abi.py, whose pointers are not memory, on a machine that has the device: it passes and launches nothing."""
+@pytest.mark.parametrize("only", ["test_abi.py -k rejects", "test_abi_layer.py"])
+def test_argument_checks_launch_nothing(fake, only):  # noqa: F811
+    """The tests of refused arguments, whose pointers are not memory, on a machine that has the device: they pass and launch
+    nothing."""
     work = os.path.join(ROOT, "_build")
     with open(os.path.join(work, "fake_runtime_plugin.py"), "w") as f:
         f.write(PLUGIN.format(fake=fake))
     env = dict(os.environ, PYTHONPATH=os.pathsep.join([work, os.environ.get("PYTHONPATH", "")]))
-    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-s", "-p", "fake_runtime_plugin", "-k", "rejects",
-                        os.path.join(ROOT, "tests", "test_abi.py")], capture_output=True, text=True, timeout=300, env=env, cwd=ROOT)
-    assert r.returncode == 0 and "1 passed" in r.stdout and "launches 0" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-s", "-p", "fake_runtime_plugin",
+                        *os.path.join(ROOT, "tests", only).split()], capture_output=True, text=True, timeout=300, env=env, cwd=ROOT)
+    assert r.returncode == 0 and " passed" in r.stdout and "launches 0\n" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
 
 
 @pytest.mark.gpu
@@ -95,3 +97,22 @@ def test_host_memory_is_refused_on_the_device():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want) and sg.sync_status() == 0
+
+
+ALLOCATOR = """
+import torch, sparse_bit_attention_smoothing_b200 as sg
+x = torch.randn(1, 2, 300, 128, device="cuda").bfloat16()
+w = torch.randn(128, 128, device="cuda").bfloat16()
+out = sg.sagesla_attn(x, x[:, :1].expand_as(x).contiguous(), x, w, topk=0.3)
+torch.cuda.synchronize()
+assert torch.isfinite(out).all() and sg.sync_status() == 0
+print("taken")
+"""
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("conf", ["expandable_segments:True", "backend:cudaMallocAsync", "backend:native"])
+def test_memory_of_every_allocator_is_known(conf):
+    env = dict(os.environ, PYTORCH_CUDA_ALLOC_CONF=conf, PYTHONPATH=ROOT)
+    r = subprocess.run([sys.executable, "-c", ALLOCATOR], capture_output=True, text=True, timeout=300, env=env, cwd=ROOT)
+    assert r.returncode == 0 and "taken" in r.stdout, r.stderr[-2000:]
